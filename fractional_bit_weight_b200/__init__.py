@@ -16,6 +16,8 @@ __all__ = [
     "whiten", "lift", "gemm_workspace_bytes", "gemm_launches", "gemm", "gemm_noalloc",
     "new_workspace",
     "device_status", "check_wait_timeout", "NOALLOC_SCRATCH_BYTES",
+    "i8_row_bytes", "quant_i8", "Norm", "norm_residual", "norm_residual_i8", "gemm_i8",
+    "gemm_i8_route", "new_i8_workspace", "GEMM_I8_WORKSPACE_BYTES",
 ]
 
 NOALLOC_SCRATCH_BYTES = 8 << 20   # LQ_NOALLOC_SCRATCH_BYTES
@@ -31,6 +33,7 @@ EXPORTS = ("lq_abi_version", "lq_lifted_bits", "lq_row_stride_bytes", "lq_pack",
            "lq_whiten", "lq_lift", "lq_gemm_workspace_bytes", "lq_gemm_launches", "lq_gemm_route",
            "lq_gemm", "lq_gemm_on_route", "lq_gemm_route_workspace_bytes", "lq_gemv_staged_plan",
            "lq_codebook_workspace_bytes", "lq_codebook_round",
+           "lq_i8_row_bytes", "lq_quant_i8", "lq_norm_residual", "lq_gemm_i8_route", "lq_gemm_i8",
            "lq_gemm_noalloc", "lq_check_wait_timeout",
            "lq_device_status", "lq_status_string", "lq_last_error")
 
@@ -44,6 +47,16 @@ class LQError(RuntimeError):
 class WhitenDesc(ctypes.Structure):
     _fields_ = [("sign", ctypes.c_void_p), ("chan_scale", ctypes.c_void_p),
                 ("block", ctypes.c_int32)]
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("eps", ctypes.c_float), ("weight", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p), ("dtype", ctypes.c_int32)]
+
+
+class GateDesc(ctypes.Structure):
+    _fields_ = [("gate", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("cols", ctypes.c_int32),
+                ("tokens", ctypes.c_int32)]
 
 
 _LIB = None
@@ -75,6 +88,15 @@ def _declare(L):
                               ctypes.c_int),
         "lq_gemm_noalloc": ([vp, ctypes.c_int, i32, dp, vp, vp, vp, ctypes.c_int, i32, i32, i32,
                              i32, vp, vp], ctypes.c_int),
+        "lq_i8_row_bytes": ([i32], i64),
+        "lq_quant_i8": ([vp, ctypes.c_int, i32, i32, i64, dp, vp, vp, vp, vp], ctypes.c_int),
+        "lq_norm_residual": ([vp, ctypes.c_int, i64, vp, ctypes.c_int, i64, i32, i32,
+                              ctypes.POINTER(NormDesc), ctypes.POINTER(GateDesc), ctypes.c_float,
+                              ctypes.c_float, vp, ctypes.POINTER(NormDesc), vp, ctypes.c_int, dp,
+                              vp, vp, vp], ctypes.c_int),
+        "lq_gemm_i8_route": ([i32, i32, i32], i32),
+        "lq_gemm_i8": ([vp, vp, i32, vp, vp, vp, i32, i32, vp, ctypes.c_int, vp, sz, i32, vp],
+                       ctypes.c_int),
         "lq_device_status": ([vp, ctypes.POINTER(i32), vp], ctypes.c_int),
         "lq_check_wait_timeout": ([vp, i32, vp], ctypes.c_int),
         "lq_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -315,6 +337,309 @@ def codebook_round(w, M, d, D, mode=0, b=None, mse=None, workspace=None, stream=
                                    workspace.numel() * workspace.element_size(), _stream(stream)),
            "lq_codebook_round")
     return M, b, mse
+
+
+# ---- 8-bit linear layers and the block boundaries around them (include/liblq.h)
+
+GEMM_I8_WORKSPACE_BYTES = 256   # LQ_GEMM_I8_WORKSPACE_BYTES
+I8_ROUTE_GEMV, I8_ROUTE_TC = 0, 1
+_F32 = (torch.float32,)
+_I8 = (torch.int8,)
+_NORM_KINDS = {"rms": 1, "layer": 2}
+
+
+def _arg(t, name, dtypes, device, shape=None):
+    """The address of a dense tensor argument, after its checks."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, expected cuda:{device}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _rows(t, name, dtypes, device=None, shape=None):
+    """(address, row stride) of a 2-D argument whose rows are dense and may lie apart."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {tuple(dtypes)}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, not {t.dim()}")
+    if device is not None and t.get_device() != device:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, expected cuda:{device}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    rows, K = t.shape
+    if t.is_contiguous():
+        return t.data_ptr(), K
+    step, unit = t.stride()
+    if (unit != 1 and K > 1) or (step < K and rows > 1):
+        raise ValueError(f"{name} must have dense rows (strides {t.stride()})")
+    return t.data_ptr(), step if rows > 1 else K
+
+
+def _elsewhere(device, stream):
+    """Whether a call on `device` has to leave the current device or stream."""
+    return stream is not None or device != torch.cuda.current_device()
+
+
+def _over_there(call, device, stream, inputs):
+    """call() with `device` and `stream` (None: that device's current one) current, so that the
+    outputs it allocates belong to the stream that writes them. The inputs' memory is kept until
+    the stream has passed the call."""
+    if stream is None:
+        with torch.cuda.device(device):
+            return call()
+    if stream.device.index != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{device}")
+    with torch.cuda.stream(stream):
+        out = call()
+        for t in inputs:
+            if isinstance(t, torch.Tensor):
+                t.record_stream(stream)
+    return out
+
+
+def _device_of(t, name):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    return t.get_device()
+
+
+def _whiten_arg(sign, chan_scale, block, K, device):
+    if not block:
+        return None
+    return ctypes.byref(WhitenDesc(
+        None if sign is None else _arg(sign, "sign", _I8, device, (K,)),
+        None if chan_scale is None else _arg(chan_scale, "chan_scale", _F32, device, (K,)),
+        int(block)))
+
+
+def i8_row_bytes(K):
+    """Bytes per row of int8 codes: K rounded up to a multiple of 16."""
+    return int(lib().lq_i8_row_bytes(K))
+
+
+def quant_i8(x, sign=None, chan_scale=None, block=0, values=False, stream=None):
+    """Symmetric int8 rows of T(x) with a scale per row (see lq_quant_i8).
+
+    x [rows][K] f32/f16/bf16; its rows may lie apart. Returns (q int8 [rows][i8_row_bytes(K)],
+    scale fp32 [rows]); with values=True also scale * q in x's type, [rows][K]."""
+    device = _device_of(x, "x")
+    if _elsewhere(device, stream):
+        return _over_there(lambda: quant_i8(x, sign, chan_scale, block, values), device, stream,
+                           (x, sign, chan_scale))
+    px, ldx = _rows(x, "x", _DTYPES)
+    rows, K = x.shape
+    q = x.new_empty((rows, (K + 15) // 16 * 16), dtype=torch.int8)
+    scale = x.new_empty(rows, dtype=torch.float32)
+    v = x.new_empty((rows, K)) if values else None
+    _check(lib().lq_quant_i8(px, _DTYPES[x.dtype], rows, K, ldx,
+                             _whiten_arg(sign, chan_scale, block, K, device), q.data_ptr(),
+                             scale.data_ptr(), v.data_ptr() if values else None,
+                             _raw_stream(device)), "lq_quant_i8")
+    return (q, scale, v) if values else (q, scale)
+
+
+def _raw_stream(device):
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
+class Norm:
+    """A norm of lq_norm_residual: kind "rms" or "layer", weight and bias [K] (f32/f16/bf16, of
+    one type) or None, eps. Holds its tensors; make it once per layer."""
+
+    def __init__(self, kind, weight=None, bias=None, eps=1e-6):
+        if kind not in _NORM_KINDS:
+            raise ValueError(f"unknown norm kind {kind!r}, expected one of {sorted(_NORM_KINDS)}")
+        self.kind, self.weight, self.bias, self.eps = kind, weight, bias, float(eps)
+        self.device = self.size = None
+        dtype = torch.float32
+        for t, name in ((weight, "weight"), (bias, "bias")):
+            if t is None:
+                continue
+            device = _device_of(t, name)
+            _arg(t, name, _DTYPES, device if self.device is None else self.device,
+                 (t.numel(),) if self.size is None else (self.size,))
+            if self.device is not None and t.dtype != dtype:
+                raise TypeError("weight and bias of a norm must have one dtype")
+            self.device, self.size, dtype = device, t.numel(), t.dtype
+        self._desc = NormDesc(_NORM_KINDS[kind], self.eps,
+                              None if weight is None else weight.data_ptr(),
+                              None if bias is None else bias.data_ptr(), _DTYPES[dtype])
+        self._ref = ctypes.byref(self._desc)
+
+    def _arg(self, K, device):
+        if self.size is not None and (self.size != K or self.device != device):
+            raise ValueError(f"norm over {self.size} entries on cuda:{self.device}, rows of {K} "
+                             f"on cuda:{device}")
+        return self._ref
+
+    def _tensors(self):
+        return self.weight, self.bias
+
+
+def _norm_arg(norm, K, device):
+    if norm is None:
+        return None
+    if not isinstance(norm, Norm):
+        raise TypeError("post and pre are Norm objects or None")
+    return norm._arg(K, device)
+
+
+def _boundary(h, residual, post, pre, gate, gate_tokens, branch_scale, residual_scale,
+              residual_out, dtype, codes, whiten):
+    """The arguments' checks, outputs and call of lq_norm_residual on the current stream."""
+    device = h.get_device()
+    ph, ldh = _rows(h, "h", _DTYPES)
+    rows, K = shape = h.shape
+    pr, ldr, rdt = None, 0, 0
+    r_out = p_out = None
+    if residual is not None:
+        pr, ldr = _rows(residual, "residual", _DTYPES, device, shape)
+        rdt = _DTYPES[residual.dtype]
+        if residual_out is None:
+            r_out = residual.new_empty(shape)
+            p_out = r_out.data_ptr()
+        elif residual_out is residual:
+            r_out, p_out = residual, pr
+        else:
+            r_out = residual_out
+            p_out = _arg(r_out, "residual_out", (residual.dtype,), device, shape)
+    elif residual_out is not None:
+        r_out = residual_out
+        p_out = _arg(r_out, "residual_out", _DTYPES, device, shape)
+        rdt = _DTYPES[r_out.dtype]
+    g = None
+    if gate is not None:
+        pg = _arg(gate, "gate", _DTYPES, device)
+        cols = gate.shape[-1] if gate.dim() == 2 else gate.numel()
+        count = gate.numel() // cols if cols else 0
+        tokens = int(gate_tokens) or (1 if count == rows else max(rows, 1))
+        if tokens < 1 or count != max(1, -(-rows // tokens)):
+            raise ValueError(f"gate of shape {tuple(gate.shape)} does not give {rows} tokens a "
+                             f"row each {tokens}")
+        g = ctypes.byref(GateDesc(pg, _DTYPES[gate.dtype], cols, tokens))
+    n = q = scale = None
+    if codes:
+        q = h.new_empty((rows, (K + 15) // 16 * 16), dtype=torch.int8)
+        scale = h.new_empty(rows, dtype=torch.float32)
+    if dtype is not None:
+        if dtype not in _DTYPES:
+            raise TypeError(f"dtype {dtype}, expected one of {tuple(_DTYPES)}")
+        n = h.new_empty(shape, dtype=dtype)
+    _check(lib().lq_norm_residual(
+        ph, _DTYPES[h.dtype], ldh, pr, rdt, ldr, rows, K, _norm_arg(post, K, device), g,
+        branch_scale, residual_scale, p_out, _norm_arg(pre, K, device),
+        None if n is None else n.data_ptr(), 0 if n is None else _DTYPES[dtype],
+        _whiten_arg(*whiten, K, device) if codes else None,
+        None if q is None else q.data_ptr(), None if scale is None else scale.data_ptr(),
+        _raw_stream(device)), "lq_norm_residual")
+    return r_out, n, q, scale
+
+
+def _boundary_inputs(h, residual, post, pre, gate, *more):
+    return (h, residual, gate, *(post._tensors() if isinstance(post, Norm) else ()),
+            *(pre._tensors() if isinstance(pre, Norm) else ()), *more)
+
+
+def norm_residual(h, residual=None, post=None, pre=None, gate=None, gate_tokens=0,
+                  branch_scale=1.0, residual_scale=1.0, residual_out=None, dtype=None,
+                  stream=None):
+    """The boundary between two blocks of a residual model (see lq_norm_residual):
+
+        c = residual_scale * residual + branch_scale * gate . post(h),   n = pre(c)
+
+    h, residual [rows][K] f32/f16/bf16, rows may lie apart; post, pre Norm or None; gate [K] or
+    [ceil(rows / gate_tokens)][K or 1], a row per gate_tokens tokens (0: one row for all, or one
+    per token if there are that many). Returns (c in residual's type, n in `dtype`, h's if None).
+    residual_out=residual updates it in place; without a residual c is only written if
+    residual_out is given (else None is returned for it)."""
+    device = _device_of(h, "h")
+    if _elsewhere(device, stream):
+        return _over_there(
+            lambda: norm_residual(h, residual, post, pre, gate, gate_tokens, branch_scale,
+                                  residual_scale, residual_out, dtype),
+            device, stream, _boundary_inputs(h, residual, post, pre, gate, residual_out))
+    r, n, _, _ = _boundary(h, residual, post, pre, gate, gate_tokens, branch_scale,
+                           residual_scale, residual_out, h.dtype if dtype is None else dtype,
+                           False, None)
+    return r, n
+
+
+def norm_residual_i8(h, residual=None, post=None, pre=None, gate=None, gate_tokens=0,
+                     branch_scale=1.0, residual_scale=1.0, residual_out=None, sign=None,
+                     chan_scale=None, block=0, dtype=None, stream=None):
+    """norm_residual with n leaving as int8 rows of T(n) and their scales, as quant_i8 makes them,
+    for gemm_i8. Returns (c, q, scale); with a dtype also n in that type."""
+    device = _device_of(h, "h")
+    if _elsewhere(device, stream):
+        return _over_there(
+            lambda: norm_residual_i8(h, residual, post, pre, gate, gate_tokens, branch_scale,
+                                     residual_scale, residual_out, sign, chan_scale, block,
+                                     dtype),
+            device, stream,
+            _boundary_inputs(h, residual, post, pre, gate, residual_out, sign, chan_scale))
+    r, n, q, scale = _boundary(h, residual, post, pre, gate, gate_tokens, branch_scale,
+                               residual_scale, residual_out, dtype, True,
+                               (sign, chan_scale, block))
+    return (r, q, scale) if dtype is None else (r, q, scale, n)
+
+
+def gemm_i8_route(batch, K, N):
+    """Which kernel lq_gemm_i8 runs for this shape (host-only query; I8_ROUTE_* codes)."""
+    return int(lib().lq_gemm_i8_route(batch, K, N))
+
+
+def new_i8_workspace(device="cuda"):
+    """A zero-filled workspace tensor for lq_gemm_i8 (its status word; see device_status)."""
+    return torch.zeros(GEMM_I8_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
+
+
+def gemm_i8(xq, xs, wq, ws, K=None, bias=None, dtype=torch.float32, y=None, workspace=None,
+            stream=None, route=None):
+    """y[t][n] = (xq[t] . wq[n]) * (xs[t] * ws[n]) + bias[n], [batch][N] of `dtype`.
+
+    xq [batch][i8_row_bytes(K)] and wq [N][i8_row_bytes(K)] int8, xs [batch], ws [N] and bias [N]
+    fp32. K None: the whole stored rows (quant_i8 pads them with zeros). route=None lets the
+    library pick the kernel; an I8_ROUTE_* code runs that one."""
+    device = _device_of(xq, "xq")
+    if _elsewhere(device, stream):
+        return _over_there(lambda: gemm_i8(xq, xs, wq, ws, K, bias, dtype, y, workspace, None,
+                                           route),
+                           device, stream, (xq, xs, wq, ws, bias, y, workspace))
+    if xq.dim() != 2 or wq.dim() != 2:
+        raise ValueError("xq and wq must have two dimensions")
+    batch, row = xq.shape
+    N = wq.shape[0]
+    if K is None:
+        K = row
+    if (K + 15) // 16 * 16 != row:
+        raise ValueError(f"rows of {row} bytes, {(K + 15) // 16 * 16} expected for K = {K}")
+    pxq = _arg(xq, "xq", _I8, device)
+    pwq = _arg(wq, "wq", _I8, device, (N, row))
+    pxs = _arg(xs, "xs", _F32, device, (batch,))
+    pws = _arg(ws, "ws", _F32, device, (N,))
+    pb = None if bias is None else _arg(bias, "bias", _F32, device, (N,))
+    if y is None:
+        if dtype not in _DTYPES:
+            raise TypeError(f"dtype {dtype}, expected one of {tuple(_DTYPES)}")
+        y = xq.new_empty((batch, N), dtype=dtype)
+    else:
+        _arg(y, "y", _DTYPES, device, (batch, N))
+    if workspace is None:
+        workspace = new_i8_workspace(xq.device)
+    pw = _arg(workspace, "workspace", (torch.uint8,), device)
+    _check(lib().lq_gemm_i8(pxq, pxs, batch, pwq, pws, pb, K, N, y.data_ptr(), _DTYPES[y.dtype],
+                            pw, workspace.numel(), -1 if route is None else route,
+                            _raw_stream(device)), "lq_gemm_i8")
+    return y
 
 
 def check_wait_timeout(workspace, limit_ms=20, stream=None):

@@ -270,6 +270,113 @@ LQ_API lq_status lq_codebook_round(const float* w, int64_t S, float* M, int32_t 
                                    int32_t mode, int8_t* b_out, double* mse, void* workspace,
                                    size_t workspace_bytes, lq_stream stream);
 
+/* ---- 8-bit linear layers and the block boundaries around them ----
+ *
+ * Not on the pages: the layers of a model that stay at 8 bits beside the fractional-bit ones,
+ * and the norms between a model's linear layers. Inference only, as the rest of the library:
+ * none of these has a gradient. */
+
+/* Bytes per row of int8 codes: K rounded up to a multiple of 16; -1 if K < 1. Rows of int8 codes
+ * are stored at this stride. lq_quant_i8 and lq_norm_residual write the padding as zero;
+ * lq_gemm_i8 ignores what it holds. */
+LQ_API int64_t lq_i8_row_bytes(int32_t K);
+/* Longest row of lq_quant_i8 and lq_norm_residual. */
+#define LQ_MAX_ROW 65536
+/* Longest row of lq_gemm_i8: every sum of K products of int8 values fits 32 bits. */
+#define LQ_MAX_I8_K 131071
+
+/* Symmetric int8 rows with a scale per row (the tokens of an activation, or the output channels
+ * of a weight matrix). With v = T(x[t]):
+ *     a = max_k |v[k]|,  scale[t] = a / 127,  q[t][k] = round(127 v[k] / a)
+ * The quotient is rounded once, half to even; q lies in -127..127. A row of zeros gives scale 0
+ * and codes 0. A row that holds an infinity or a NaN gives scale NaN and codes 0, so that it
+ * reads NaN behind lq_gemm_i8.
+ *   x       [rows][K] device, row t at element t * ldx (ldx >= K).
+ *   T       as for lq_gemm (NULL = identity).
+ *   q       [rows][lq_i8_row_bytes(K)] int8 device, 16-byte aligned.
+ *   scale   [rows] fp32 device.
+ *   values  [rows][K] of x's type, dense, or NULL: scale * q, what the codes stand for.
+ * Errors: LQ_EINVAL (null or misaligned pointers, rows < 0, K < 1, ldx < K, unknown dtype, bad T),
+ * LQ_EUNSUPPORTED (K > LQ_MAX_ROW, Hadamard block > LQ_MAX_HADAMARD), LQ_ECUDA. rows = 0 is a
+ * no-op. */
+LQ_API lq_status lq_quant_i8(const void* x, lq_dtype xdt, int32_t rows, int32_t K, int64_t ldx,
+                             const lq_whiten_desc* T, int8_t* q, float* scale, void* values,
+                             lq_stream stream);
+
+/* A norm over the K entries of a row; statistics in fp32.
+ *   LQ_NORM_RMS:   v / sqrt(mean(v^2) + eps) * weight + bias
+ *   LQ_NORM_LAYER: (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps) * weight + bias */
+typedef enum lq_norm_kind { LQ_NORM_RMS = 1, LQ_NORM_LAYER = 2 } lq_norm_kind;
+typedef struct lq_norm_desc {
+  int32_t kind;        /* an lq_norm_kind */
+  float eps;           /* >= 0 and finite */
+  const void* weight;  /* [K] device or NULL (all 1) */
+  const void* bias;    /* [K] device or NULL (all 0) */
+  int32_t dtype;       /* lq_dtype of weight and bias */
+} lq_norm_desc;
+
+/* A gate on the branch: token t takes row t / tokens of gate [ceil(rows / tokens)][cols]. */
+typedef struct lq_gate_desc {
+  const void* gate;    /* device */
+  int32_t dtype;       /* lq_dtype */
+  int32_t cols;        /* K: one factor per channel; 1: one for the whole row */
+  int32_t tokens;      /* tokens that share a gate row: 1 = a row per token, >= rows = one row */
+} lq_gate_desc;
+
+/* The boundary between two blocks of a residual model, in one pass over the rows:
+ *     u = post(h[t])                                          (post NULL: u = h[t])
+ *     c = residual_scale * r[t] + branch_scale * gate(t) . u  (gate NULL: 1; r NULL: no first term)
+ *     n = pre(c)                                              (pre NULL: n = c)
+ * c and n are held in fp32; each output is rounded from them once (n does not see the rounding
+ * of r_out).
+ *   h      [rows][K] device, row t at element t * ldh (ldh >= K): the block's output.
+ *   r      [rows][K] device, row t at element t * ldr (ldr >= K), or NULL.
+ *   r_out  [rows][K] of type rdt: c, or NULL. Dense, unless r_out == r: then in place at r's
+ *          stride. No other output may overlap an input.
+ *   n_out  [rows][K] of type ndt, dense: n, or NULL.
+ *   q, q_scale  T(n) as int8 rows and scales exactly as lq_quant_i8 makes them, or both NULL
+ *          (T is then not used).
+ * Errors: LQ_EINVAL (null or misaligned pointers, no output at all, q without q_scale, rows < 0,
+ * K < 1, strides < K, unknown dtype or norm kind, bad eps, gate cols or tokens, bad T),
+ * LQ_EUNSUPPORTED (K > LQ_MAX_ROW, Hadamard block > LQ_MAX_HADAMARD), LQ_ECUDA. rows = 0 is a
+ * no-op. */
+LQ_API lq_status lq_norm_residual(const void* h, lq_dtype hdt, int64_t ldh, const void* r,
+                                  lq_dtype rdt, int64_t ldr, int32_t rows, int32_t K,
+                                  const lq_norm_desc* post, const lq_gate_desc* gate,
+                                  float branch_scale, float residual_scale, void* r_out,
+                                  const lq_norm_desc* pre, void* n_out, lq_dtype ndt,
+                                  const lq_whiten_desc* T, int8_t* q, float* q_scale,
+                                  lq_stream stream);
+
+/* Kernel routes of lq_gemm_i8. */
+#define LQ_I8_ROUTE_GEMV 0  /* warp-level int8 MMA, up to LQ_I8_GEMV_MAX_BATCH tokens */
+#define LQ_I8_ROUTE_TC 1    /* tcgen05 kind::i8 tiles, any batch */
+#define LQ_I8_GEMV_MAX_BATCH 32
+/* Bytes of the lq_gemm_i8 workspace: the status word. */
+#define LQ_GEMM_I8_WORKSPACE_BYTES 256
+
+/* Which kernel lq_gemm_i8 runs for this shape (LQ_I8_ROUTE_*; host-only query). Returns -1 on
+ * invalid sizes. */
+LQ_API int32_t lq_gemm_i8_route(int32_t batch, int32_t K, int32_t N);
+
+/* Matrix product in 8-bit integers with a scale per token and per output channel:
+ *     y[t][n] = (sum_k xq[t][k] wq[n][k]) * (xs[t] * ws[n]) + bias[n]
+ * The sum is an exact int32 (entries may be -128..127), scaled in fp32 and rounded to y's type
+ * once.
+ *   xq [batch][lq_i8_row_bytes(K)], wq [N][lq_i8_row_bytes(K)] int8 device, 16-byte aligned.
+ *   xs [batch], ws [N] fp32 device; bias [N] fp32 device or NULL.
+ *   y  [batch][N] of type ydt, dense.
+ *   workspace: LQ_GEMM_I8_WORKSPACE_BYTES bytes, 256-byte aligned, zero-filled once before its
+ *   first use; holds the status word that lq_device_status reads.
+ *   route: -1 lets the library choose, an LQ_I8_ROUTE_* code asks for that kernel.
+ * Errors: LQ_EINVAL (null or misaligned pointers, batch < 0, N < 0, K < 1, unknown dtype or
+ * route, workspace too small), LQ_EUNSUPPORTED (K > LQ_MAX_I8_K, a route that does not take the
+ * batch), LQ_ECUDA. batch = 0 or N = 0 is a no-op. */
+LQ_API lq_status lq_gemm_i8(const int8_t* xq, const float* xs, int32_t batch, const int8_t* wq,
+                            const float* ws, const float* bias, int32_t K, int32_t N, void* y,
+                            lq_dtype ydt, void* workspace, size_t workspace_bytes, int32_t route,
+                            lq_stream stream);
+
 /* Synchronise `stream`, then read the workspace status word into *code (0 = no device-side
  * failure) and clear it. Returns LQ_OK, or the lq_status that the word records. */
 LQ_API lq_status lq_device_status(void* workspace, int32_t* code, lq_stream stream);
