@@ -1,18 +1,21 @@
 // lq_rows.cu -- lq_quant_i8 and lq_norm_residual: one pass over the rows of an activation.
 //
-// A row of the residual stream, its norms, its whitening T and its int8 codes need three or more
-// reductions over the same K entries (sum of squares, mean, largest magnitude). One CTA takes one
-// row and keeps it in registers as fp32 between them, so each input is read once and each output
-// written once; the reductions are warp shuffles and one shared-memory exchange each. A thread
-// holds NV vectors of eight consecutive entries, vector j of thread i at column
-// 8 * (j * threads + i): a warp's 32 vectors are 256 consecutive entries, so a Hadamard block of
-// up to 256 inputs runs in one warp's registers and shuffles.
+// A row of the residual stream, its norms, its whitening T and its int8 codes need up to five
+// reductions over the same K entries (sums, sums of squares, largest magnitude). A row stays in
+// registers as fp32 between them, so each input is read once and each output written once. One CTA
+// takes a row of up to 8192 entries, a cluster of up to eight CTAs a longer one; a reduction is
+// warp shuffles and one exchange through the (cluster's) shared memory.
+//
+// A thread holds NV vectors of eight consecutive entries, vector j of thread i at column
+// 8 * (j * threads + i) of the CTA's part: a warp's 32 vectors are 256 consecutive entries, so a
+// Hadamard block of up to 256 inputs runs in one warp's registers and shuffles.
 //
 // What bounds it: HBM for many rows (bytes per entry: h + r + r_out + n or the codes), the latency
 // of load -> reductions -> store for a few.
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <type_traits>
 
 #include "lq_device.cuh"
 
@@ -44,9 +47,63 @@ struct RowArgs {
   Whiten T;
 };
 
-struct F32 { static constexpr int dt = LQ_F32; };
-struct F16 { static constexpr int dt = LQ_F16; };
-struct BF16 { static constexpr int dt = LQ_BF16; };
+struct F32 {
+  static constexpr int dt = LQ_F32, size = 4;
+  typedef float type;
+};
+struct F16 {
+  static constexpr int dt = LQ_F16, size = 2;
+  typedef __half type;
+};
+struct BF16 {
+  static constexpr int dt = LQ_BF16, size = 2;
+  typedef __nv_bfloat16 type;
+};
+struct None { static constexpr int dt = -1, size = 2; };
+
+// f with the type that dt names. Loops over a thread's entries go inside f: as a branch around a
+// whole loop the choice costs nothing, inside it the compiler evaluates every type and selects.
+template <class F>
+__device__ __forceinline__ void with_type(int dt, F f) {
+  if (dt == LQ_BF16) f(BF16{});
+  else if (dt == LQ_F16) f(F16{});
+  else f(F32{});
+}
+
+// Two fp32 operations in one instruction, on entries 2i and 2i + 1 of a vector.
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
+  float2 r;
+  asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " mov.b64 c, {%6, %7};\n fma.rn.f32x2 a, a, b, c;\n mov.b64 {%0, %1}, a;\n}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(z.x), "f"(z.y));
+  return r;
+}
+
+__device__ __forceinline__ float2 mul2(float2 x, float2 y) {
+  float2 r;
+  asm("{\n .reg .b64 a, b;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " mul.rn.f32x2 a, a, b;\n mov.b64 {%0, %1}, a;\n}"
+      : "=f"(r.x), "=f"(r.y) : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+  return r;
+}
+
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+  float2 r;
+  asm("{\n .reg .b64 a, b;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " add.rn.f32x2 a, a, b;\n mov.b64 {%0, %1}, a;\n}"
+      : "=f"(r.x), "=f"(r.y) : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+  return r;
+}
+
+__device__ __forceinline__ float2 pair(const float (&v)[8], int i) {
+  return make_float2(v[2 * i], v[2 * i + 1]);
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ void put(float (&v)[8], int i, float2 x) {
+  v[2 * i] = x.x;
+  v[2 * i + 1] = x.y;
+}
 
 // 16 bytes that are read once: not kept in L1, where the norms' weights live
 __device__ __forceinline__ uint4 ld_stream(const void* p) {
@@ -56,8 +113,9 @@ __device__ __forceinline__ uint4 ld_stream(const void* p) {
   return v;
 }
 
-__device__ __forceinline__ void unpack2(uint32_t w, int dt, float& lo, float& hi) {
-  if (dt == LQ_BF16) {
+template <class DT>
+__device__ __forceinline__ void unpack2(uint32_t w, float& lo, float& hi) {
+  if constexpr (DT::dt == LQ_BF16) {
     lo = __uint_as_float(w << 16);
     hi = __uint_as_float(w & 0xffff0000u);
   } else {
@@ -67,98 +125,216 @@ __device__ __forceinline__ void unpack2(uint32_t w, int dt, float& lo, float& hi
   }
 }
 
-__device__ __forceinline__ void unpack8(const uint4& a, const uint4& b, int dt, float (&v)[8]) {
-  if (dt == LQ_F32) {
+template <class DT>
+__device__ __forceinline__ void unpack8(const uint4& a, const uint4& b, float (&v)[8]) {
+  if constexpr (DT::dt == LQ_F32) {
     v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y);
     v[2] = __uint_as_float(a.z); v[3] = __uint_as_float(a.w);
     v[4] = __uint_as_float(b.x); v[5] = __uint_as_float(b.y);
     v[6] = __uint_as_float(b.z); v[7] = __uint_as_float(b.w);
   } else {
-    unpack2(a.x, dt, v[0], v[1]);
-    unpack2(a.y, dt, v[2], v[3]);
-    unpack2(a.z, dt, v[4], v[5]);
-    unpack2(a.w, dt, v[6], v[7]);
+    unpack2<DT>(a.x, v[0], v[1]);
+    unpack2<DT>(a.y, v[2], v[3]);
+    unpack2<DT>(a.z, v[4], v[5]);
+    unpack2<DT>(a.w, v[6], v[7]);
   }
 }
 
-// entries [c, c + 8) of a vector that every row reads (a norm's weight, a gate), as fp32
-template <bool VEC>
-__device__ __forceinline__ void load_shared8(const void* p, int dt, int64_t c, int n,
-                                             float (&v)[8]) {
-  if (VEC) {
-    const uint4* s = reinterpret_cast<const uint4*>(static_cast<const char*>(p) +
-                                                    c * (dt == LQ_F32 ? 4 : 2));
-    const uint4 a = __ldg(s);
-    const uint4 b = dt == LQ_F32 ? __ldg(s + 1) : a;
-    unpack8(a, b, dt, v);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = e < n ? load_as_f32(p, dt, c + e) : 0.f;
-  }
-}
-
-__device__ __forceinline__ uint32_t pack2(float lo, float hi, int dt) {
-  if (dt == LQ_BF16) {
+template <class DT>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if constexpr (DT::dt == LQ_BF16) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
   }
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// entries [i, i + n) of an output, each rounded once
-template <bool VEC>
-__device__ __forceinline__ void store8(void* p, int dt, int64_t i, int n, const float (&v)[8]) {
-  if (VEC) {
-    uint4* d = reinterpret_cast<uint4*>(static_cast<char*>(p) + i * (dt == LQ_F32 ? 4 : 2));
-    if (dt == LQ_F32) {
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void from_f32(float v, float& x) { x = v; }
+__device__ __forceinline__ void from_f32(float v, __half& x) { x = __float2half_rn(v); }
+__device__ __forceinline__ void from_f32(float v, __nv_bfloat16& x) { x = __float2bfloat16_rn(v); }
+
+// How the entries of a row map to threads and how they move.
+//   kVec     16-byte accesses: K a multiple of 8, everything aligned
+//   kStrided any K and alignment, no whitening: a warp's 256 entries are dealt out one by one, so
+//            that its 2- and 4-byte accesses fall on consecutive addresses
+//   kScalar  any K and alignment with whitening, whose butterflies want eight consecutive entries
+//            per thread
+//   kFull    kVec without a ragged end: the CTAs of a row cover exactly K entries
+enum Mode { kVec, kStrided, kScalar, kFull };
+__host__ __device__ constexpr bool is_vec(Mode m) { return m == kVec || m == kFull; }
+
+// whether column c of a part of n columns is there
+template <Mode M>
+__device__ __forceinline__ bool in_row(int c, int n) { return M == kFull || c < n; }
+
+// column of entry e of vector j of this thread, within the CTA's part of the row
+template <Mode M>
+__device__ __forceinline__ int col_of(int j, int e) {
+  const int base = 8 * (j * (int)blockDim.x);
+  if (M == kStrided) return base + 8 * (int)(threadIdx.x & ~31u) + 32 * e + (int)(threadIdx.x & 31);
+  return base + 8 * (int)threadIdx.x + e;
+}
+
+// v = entries of vector j of the row part at element `off` of p, zero from column n on
+template <class DT, Mode M>
+__device__ __forceinline__ void load_scalar(const void* p, int64_t off, int j, int n,
+                                            float (&v)[8]) {
+  const typename DT::type* q = static_cast<const typename DT::type*>(p) + off;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int c = col_of<M>(j, e);
+    v[e] = c < n ? to_f32(q[c]) : 0.f;
+  }
+}
+
+// the same for a vector that every row reads (a norm's weight, a gate); L1 keeps it
+template <class DT, Mode M>
+__device__ __forceinline__ void load_shared8(const void* p, int64_t off, int j, int n,
+                                             float (&v)[8]) {
+  if constexpr (is_vec(M)) {
+    const uint4* s = reinterpret_cast<const uint4*>(static_cast<const typename DT::type*>(p) + off +
+                                                    col_of<M>(j, 0));
+    const uint4 a = __ldg(s);
+    unpack8<DT>(a, DT::size == 4 ? __ldg(s + 1) : a, v);
+  } else {
+    load_scalar<DT, M>(p, off, j, n, v);
+  }
+}
+
+// entries of vector j of an output row part at element `off` of p, each rounded once
+template <class DT, Mode M>
+__device__ __forceinline__ void store8(void* p, int64_t off, int j, int n, const float (&v)[8]) {
+  typename DT::type* q = static_cast<typename DT::type*>(p) + off;
+  if constexpr (is_vec(M)) {
+    uint4* d = reinterpret_cast<uint4*>(q + col_of<M>(j, 0));
+    if constexpr (DT::size == 4) {
       d[0] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
                         __float_as_uint(v[3]));
       d[1] = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]),
                         __float_as_uint(v[7]));
     } else {
-      d[0] = make_uint4(pack2(v[0], v[1], dt), pack2(v[2], v[3], dt), pack2(v[4], v[5], dt),
-                        pack2(v[6], v[7], dt));
+      d[0] = make_uint4(pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]),
+                        pack2<DT>(v[6], v[7]));
     }
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      if (e < n) {
-        if (dt == LQ_F32) static_cast<float*>(p)[i + e] = v[e];
-        else if (dt == LQ_F16) static_cast<__half*>(p)[i + e] = __float2half_rn(v[e]);
-        else static_cast<__nv_bfloat16*>(p)[i + e] = __float2bfloat16_rn(v[e]);
-      }
+      if (col_of<M>(j, e) < n) from_f32(v[e], q[col_of<M>(j, e)]);
   }
 }
 
-// Sum over the CTA; `red` holds 32 words and is not the one of the reduction before.
-__device__ __forceinline__ float cta_sum(float x, float* red) {
+// v = op(v, entries of the shared vector p), two entries at a time
+template <int NV, Mode M, class Op>
+__device__ __forceinline__ void combine(float (&v)[NV][8], const void* p, int dt, int64_t off, int n,
+                                        Op op) {
+  with_type(dt, [&](auto t) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  if (blockDim.x == 32) return x;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (lane == 0) red[warp] = x;
-  __syncthreads();
-  x = lane < (int)(blockDim.x >> 5) ? red[lane] : 0.f;
+    for (int j = 0; j < NV; ++j) {
+      if (!in_row<M>(col_of<M>(j, 0), n)) continue;
+      float w[8];
+      load_shared8<decltype(t), M>(p, off, j, n, w);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
+      for (int i = 0; i < 4; ++i) put(v[j], i, op(pair(v[j], i), pair(w, i)));
+    }
+  });
 }
 
-__device__ __forceinline__ uint32_t cta_max(uint32_t x, float* red) {
-  x = __reduce_max_sync(0xffffffffu, x);
-  if (blockDim.x == 32) return x;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (lane == 0) red[warp] = __uint_as_float(x);
-  __syncthreads();
-  x = lane < (int)(blockDim.x >> 5) ? __float_as_uint(red[lane]) : 0u;
-  return __reduce_max_sync(0xffffffffu, x);
+template <int NV, Mode M>
+__device__ __forceinline__ void store_all(const float (&v)[NV][8], void* p, int dt, int64_t off,
+                                          int n) {
+  with_type(dt, [&](auto t) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (in_row<M>(col_of<M>(j, 0), n)) store8<decltype(t), M>(p, off, j, n, v[j]);
+  });
 }
 
-// v = norm(v), in place. Entries past K are zero before and after.
-template <int NV, bool VEC>
-__device__ __forceinline__ void apply_norm(float (&v)[NV][8], const NormArgs& p, int K,
-                                           float* red0, float* red1) {
+// the larger magnitude, NaN if either is
+__device__ __forceinline__ float max_abs(float a, float b) {
+  float m;
+  asm("{\n .reg .f32 t;\n abs.f32 t, %2;\n max.NaN.f32 %0, %1, t;\n}" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
+
+// Reductions over a row: every warp leaves its partial in the shared memory of all the row's CTAs,
+// then all threads read all partials. Each reduction has its own slots, so none waits for the one
+// before to be read.
+struct Reducer {
+  uint32_t* slots;   // [kReductions][8 CTAs][32 warps]
+  int ctas, rank;
+
+  __device__ __forceinline__ void put(int which, uint32_t x) const {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    uint32_t* mine = slots + which * 256 + rank * 32 + warp;
+    // zeros behind the last warp, up to the four slots of one read
+    const int pad = warp == warps - 1 ? -warps & 3 : 0;
+    if (ctas == 1) {
+      if (lane <= pad) mine[lane] = lane == 0 ? x : 0u;
+      __syncthreads();
+      return;
+    }
+    for (int p = 0; p <= pad; ++p) {
+      if (lane < ctas) {
+        uint32_t addr;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                     : "=r"(addr) : "r"((uint32_t)__cvta_generic_to_shared(mine + p)), "r"(lane));
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(p == 0 ? x : 0u)
+                     : "memory");
+      }
+    }
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;"
+                 ::: "memory");
+  }
+
+  template <class F>
+  __device__ __forceinline__ void each(int which, F f) const {
+    const int quads = ((blockDim.x >> 5) + 3) >> 2;
+    for (int c = 0; c < ctas; ++c)
+      for (int i = 0; i < quads; ++i)
+        f(*reinterpret_cast<const uint4*>(slots + which * 256 + c * 32 + 4 * i));
+  }
+
+  __device__ __forceinline__ float sum(int which, float x) const {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    if (blockDim.x == 32 && ctas == 1) return x;
+    put(which, __float_as_uint(x));
+    x = 0.f;
+    each(which, [&](uint4 p) {
+      x += (__uint_as_float(p.x) + __uint_as_float(p.y)) +
+           (__uint_as_float(p.z) + __uint_as_float(p.w));
+    });
+    return x;
+  }
+
+  __device__ __forceinline__ uint32_t max(int which, uint32_t x) const {
+    x = __reduce_max_sync(0xffffffffu, x);
+    if (blockDim.x == 32 && ctas == 1) return x;
+    put(which, x);
+    x = 0u;
+    each(which, [&](uint4 p) { x = ::max(::max(x, ::max(p.x, p.y)), ::max(p.z, p.w)); });
+    return x;
+  }
+};
+
+template <int NV>
+__device__ __forceinline__ void scale_all(float (&v)[NV][8], float f) {
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) put(v[j], i, mul2(pair(v[j], i), both(f)));
+}
+
+// v = norm(v), in place. Entries from column n of this CTA's part on are zero before and after.
+// first: this norm's two reductions are `first` and `first + 1`.
+template <int NV, Mode M>
+__device__ __forceinline__ void apply_norm(float (&v)[NV][8], const NormArgs& p, int K, int n,
+                                           int64_t off, const Reducer& red, int first) {
   const float inv_k = 1.f / (float)K;
   if (p.kind == LQ_NORM_LAYER) {
     float s = 0.f;
@@ -166,69 +342,57 @@ __device__ __forceinline__ void apply_norm(float (&v)[NV][8], const NormArgs& p,
     for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int e = 0; e < 8; ++e) s += v[j][e];
-    const float mean = cta_sum(s, red1) * inv_k;
+    const float mean = red.sum(first + 1, s) * inv_k;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int n = K - 8 * (int)(j * blockDim.x + threadIdx.x);
+    for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (e < n) v[j][e] -= mean;
-    }
+        if (in_row<M>(col_of<M>(j, e), n)) v[j][e] -= mean;
   }
-  float ss = 0.f;
+  float2 ss = both(0.f);
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(v[j][e], v[j][e], ss);
-  const float rs = 1.f / sqrtf(fmaf(cta_sum(ss, red0), inv_k, p.eps));
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int c = 8 * (j * blockDim.x + threadIdx.x);
-    if (c >= K) continue;
-    float w[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[j][e] *= rs;
-    if (p.w) {
-      load_shared8<VEC>(p.w, p.dt, c, K - c, w);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[j][e] *= w[e];
-    }
-    if (p.b) {
-      load_shared8<VEC>(p.b, p.dt, c, K - c, w);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[j][e] += w[e];
-    }
+    for (int i = 0; i < 4; ++i) ss = fma2(pair(v[j], i), pair(v[j], i), ss);
+  const float rs = rsqrtf(fmaf(red.sum(first, ss.x + ss.y), inv_k, p.eps));
+  if (p.w) {
+    combine<NV, M>(v, p.w, p.dt, off, n,
+                   [&](float2 x, float2 w) { return mul2(mul2(x, both(rs)), w); });
+  } else {
+    scale_all<NV>(v, rs);
   }
+  if (p.b) combine<NV, M>(v, p.b, p.dt, off, n, [](float2 x, float2 w) { return add2(x, w); });
 }
 
-// v = T(v): sign and channel scale, then butterflies over distance 1, 2, 4 in a thread's vector,
-// 8 .. 128 across the warp's lanes, 256 and up through shared memory (ex: 8 * threads floats).
-template <int NV, bool VEC>
-__device__ __forceinline__ void apply_whiten(float (&v)[NV][8], const Whiten& T, int K, float* ex) {
+// v = sqrt(block) T(v): sign and channel scale, then butterflies over distance 1, 2, 4 in a
+// thread's vector, 8 .. 128 across the warp's lanes, 256 and up through shared memory (ex:
+// 8 * threads floats). The codes do not see a common factor and the scale takes it later.
+template <int NV, Mode M>
+__device__ __forceinline__ void apply_whiten(float (&v)[NV][8], const Whiten& T, int n, int64_t off,
+                                             float* ex) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int c = 8 * (j * blockDim.x + threadIdx.x);
-    const int n = K - c;
-    if (n > 0) {
+    const int c = col_of<M>(j, 0);
+    if (in_row<M>(c, n)) {
       if (T.chan_scale) {
         float cs[8];
-        load_shared8<VEC>(T.chan_scale, LQ_F32, c, n, cs);
+        load_shared8<F32, M>(T.chan_scale, off, j, n, cs);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[j][e] *= cs[e];
       }
       if (T.sign) {
         uint32_t lo, hi;
-        if (VEC) {
-          const uint2 s = __ldg(reinterpret_cast<const uint2*>(T.sign + c));
+        if (is_vec(M)) {
+          const uint2 s = __ldg(reinterpret_cast<const uint2*>(T.sign + off + c));
           lo = s.x;
           hi = s.y;
         } else {
           lo = hi = 0;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            if (e < n) lo |= (uint32_t)(uint8_t)T.sign[c + e] << (8 * e);
-            if (e + 4 < n) hi |= (uint32_t)(uint8_t)T.sign[c + e + 4] << (8 * e);
+            if (c + e < n) lo |= (uint32_t)(uint8_t)T.sign[off + c + e] << (8 * e);
+            if (c + e + 4 < n) hi |= (uint32_t)(uint8_t)T.sign[off + c + e + 4] << (8 * e);
           }
         }
 #pragma unroll
@@ -240,40 +404,50 @@ __device__ __forceinline__ void apply_whiten(float (&v)[NV][8], const Whiten& T,
         }
       }
     }
+    const float2 minus = both(-1.f);
+    if (T.block > 1) {
 #pragma unroll
-    for (int h = 1; h < 8; h <<= 1)
-      if (h < T.block)
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if ((e & h) == 0) {
-            const float a = v[j][e], b = v[j][e + h];
-            v[j][e] = a + b;
-            v[j][e + h] = a - b;
-          }
-    for (int m = 1; m < 32 && 8 * m < T.block; m <<= 1) {
-      const bool upper = (lane & m) != 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float o = __shfl_xor_sync(0xffffffffu, v[j][e], m);
-        v[j][e] = upper ? o - v[j][e] : v[j][e] + o;
-      }
+      for (int i = 0; i < 4; ++i)
+        put(v[j], i, make_float2(v[j][2 * i] + v[j][2 * i + 1], v[j][2 * i] - v[j][2 * i + 1]));
     }
-    // the vectors j of the CTA's threads are 8 * threads consecutive entries, a whole number of
-    // blocks
-    for (int m = 32; 8 * m < T.block; m <<= 1) {
+#pragma unroll
+    for (int h = 1; h < 4; h <<= 1)
+      if (2 * h < T.block)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if ((i & h) == 0) {
+            const float2 x = pair(v[j], i), y = pair(v[j], i + h);
+            put(v[j], i, add2(x, y));
+            put(v[j], i + h, fma2(y, minus, x));
+          }
+  }
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    if (8 * m >= T.block) break;
+    const float2 s = both((lane & m) != 0 ? -1.f : 1.f);
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 o = make_float2(__shfl_xor_sync(0xffffffffu, v[j][2 * i], m),
+                                     __shfl_xor_sync(0xffffffffu, v[j][2 * i + 1], m));
+        put(v[j], i, fma2(pair(v[j], i), s, o));
+      }
+  }
+  // the vectors j of the CTA's threads are 8 * threads consecutive entries, a whole number of
+  // blocks
+  for (int m = 32; 8 * m < T.block; m <<= 1) {
+    const float s = (threadIdx.x & m) != 0 ? -1.f : 1.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
       __syncthreads();
 #pragma unroll
       for (int e = 0; e < 8; ++e) ex[e * blockDim.x + threadIdx.x] = v[j][e];
       __syncthreads();
-      const bool upper = (threadIdx.x & m) != 0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float o = ex[e * blockDim.x + (threadIdx.x ^ m)];
-        v[j][e] = upper ? o - v[j][e] : v[j][e] + o;
-      }
+      for (int e = 0; e < 8; ++e)
+        v[j][e] = fmaf(v[j][e], s, ex[e * blockDim.x + (threadIdx.x ^ m)]);
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[j][e] *= T.inv_sqrt;
   }
 }
 
@@ -287,192 +461,259 @@ __device__ __forceinline__ float border_code(float u, float a, float m) {
   return d > 0.f || (d == 0.f && odd) ? m + 1.f : m;
 }
 
-// Codes of eight entries: bytes lo (entries 0..3) and hi (4..7). t = v * (127 / a) is off by at
-// most 127 * 2^-23 from the quotient, so rounding it is right unless it lies within 1e-4 of a
-// border; there border_code decides.
-__device__ __forceinline__ void codes8(const float (&v)[8], float inv, float a, uint32_t& lo,
-                                       uint32_t& hi) {
-  constexpr float kRound = 12582912.f;   // 1.5 * 2^23: adding it rounds half to even
-  uint32_t b[8];
+constexpr float kRound = 12582912.f;   // 1.5 * 2^23: adding it rounds half to even
+
+// Codes of eight entries as b[e] = bits of kRound + code (the low byte is the code). fma(v, 127 / a,
+// kRound) rounds a quotient that is off by at most 127 * 2^-24, so the code is right unless the
+// quotient lies within 1e-4 of a border; there border_code decides.
+__device__ __forceinline__ void codes8(const float (&v)[8], float inv, float a, uint32_t (&b)[8]) {
+  const float2 f = both(inv), one = both(kRound), minus = both(-1.f);
   float worst = 0.f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float t = v[e] * inv;
-    const float m = t + kRound;
-    b[e] = __float_as_uint(m);           // low byte: the code
-    worst = fmaxf(worst, fabsf(t - (m - kRound)));
+  for (int i = 0; i < 4; ++i) {
+    const float2 m = fma2(pair(v, i), f, one);
+    const float2 d = fma2(pair(v, i), f, fma2(m, minus, one));
+    b[2 * i] = __float_as_uint(m.x);
+    b[2 * i + 1] = __float_as_uint(m.y);
+    worst = fmaxf(worst, fmaxf(fabsf(d.x), fabsf(d.y)));
   }
-  if (worst > 0.4999f) {
-#pragma unroll 1
+  if (worst > 0.49998f) {
+#pragma unroll
     for (int e = 0; e < 8; ++e) {
-      float ve = v[0];
-#pragma unroll
-      for (int i = 1; i < 8; ++i) ve = e == i ? v[i] : ve;
-      const float t = fabsf(ve * inv), m = floorf(t);
-      if (fabsf(t - m - 0.5f) < 1.1e-4f) {
-        const float c = copysignf(border_code(fabsf(ve), a, m), ve);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) b[i] = e == i ? (uint32_t)(int)c : b[i];
+      const float m = __uint_as_float(b[e]);
+      if (fabsf(fmaf(v[e], inv, kRound - m)) > 0.49998f) {
+        const float below = floorf(fabsf(v[e] * inv));
+        b[e] = __float_as_uint(kRound + copysignf(border_code(fabsf(v[e]), a, below), v[e]));
       }
     }
   }
-  lo = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
-  hi = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
 }
 
-template <class HT, class RT, int NV, bool VEC, int kMaxThreads>
-__global__ void __launch_bounds__(kMaxThreads, 1) row_kernel(const __grid_constant__ RowArgs a) {
-  extern __shared__ __align__(16) float ex[];   // whitening blocks over 256
-  __shared__ float red[4][32];
-  const int K = a.K, tid = threadIdx.x, T = blockDim.x;
-  const int64_t row = blockIdx.x;
-  const int hdt = VEC ? HT::dt : a.hdt, rdt = VEC ? RT::dt : a.rdt;
-  float v[NV][8];
+__device__ __forceinline__ uint32_t low_bytes(uint32_t b0, uint32_t b1, uint32_t b2, uint32_t b3) {
+  return __byte_perm(__byte_perm(b0, b1, 0x0040), __byte_perm(b2, b3, 0x0040), 0x5410);
+}
 
-  if (VEC) {
-    uint4 hr[NV][HT::dt == LQ_F32 ? 2 : 1];
-    const char* hp = static_cast<const char*>(a.h) + row * a.ldh * (HT::dt == LQ_F32 ? 4 : 2);
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = 8 * (j * T + tid);
-      if (c < K) {
-        hr[j][0] = ld_stream(hp + (int64_t)c * (HT::dt == LQ_F32 ? 4 : 2));
-        if (HT::dt == LQ_F32) hr[j][HT::dt == LQ_F32 ? 1 : 0] = ld_stream(hp + (int64_t)c * 4 + 16);
-      } else {
-        hr[j][0] = make_uint4(0u, 0u, 0u, 0u);
-        if (HT::dt == LQ_F32) hr[j][HT::dt == LQ_F32 ? 1 : 0] = make_uint4(0u, 0u, 0u, 0u);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < NV; ++j) unpack8(hr[j][0], hr[j][HT::dt == LQ_F32 ? 1 : 0], HT::dt, v[j]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = 8 * (j * T + tid);
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        v[j][e] = c + e < K ? load_as_f32(a.h, hdt, row * a.ldh + c + e) : 0.f;
-    }
-  }
+// The most threads of a CTA and the CTAs an SM should hold. The wide form (NV = 1) is for calls
+// whose CTAs are all resident at once, where the latency of a row counts; the other keeps a CTA
+// small, so that several rows are in flight per SM: 64 registers a thread without a residual, 80
+// with one (64 spill: 2048 x 8192 took 37.2 against 34.4 us).
+template <int NV, bool kHasR>
+struct Form {
+  static constexpr int kThreads = NV == 1 ? 1024 : 256;
+  static constexpr int kBlocks = NV == 1 ? 1 : kHasR ? 3 : 4;
+};
+constexpr int kReductions = 5;
 
-  if (a.post.kind) apply_norm<NV, VEC>(v, a.post, K, red[0], red[1]);
-
-  if (a.gate) {
-    const int64_t g = (row / a.gate_tokens) * a.gate_cols;
-    if (a.gate_cols == K && K > 1) {
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int c = 8 * (j * T + tid);
-        if (c >= K) continue;
-        float w[8];
-        load_shared8<VEC>(a.gate, a.gdt, g + c, K - c, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[j][e] *= w[e];
-      }
-    } else {
-      const float w = load_as_f32(a.gate, a.gdt, g);
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[j][e] *= w;
-    }
-  }
+template <class DT, int NV, Mode M>
+__device__ __forceinline__ void load_raw(uint4 (&raw)[NV][DT::size / 2], const void* p,
+                                         int64_t first, int n) {
+  const char* src = static_cast<const char*>(p) + first * DT::size;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int c = 8 * (j * T + tid);
-    if (c >= K) continue;
+    const int c = col_of<kVec>(j, 0);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[j][e] *= a.branch;
-    if (a.r) {
-      float w[8];
-      if (VEC) {
-        const char* rp = static_cast<const char*>(a.r) +
-                         (row * a.ldr + c) * (RT::dt == LQ_F32 ? 4 : 2);
-        const uint4 r0 = ld_stream(rp);
-        unpack8(r0, RT::dt == LQ_F32 ? ld_stream(rp + 16) : r0, RT::dt, w);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          w[e] = c + e < K ? load_as_f32(a.r, rdt, row * a.ldr + c + e) : 0.f;
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[j][e] = fmaf(a.resid, w[e], v[j][e]);
-    }
-    if (a.r_out) store8<VEC>(a.r_out, rdt, row * a.ldro + c, K - c, v[j]);
+    for (int i = 0; i < DT::size / 2; ++i)
+      raw[j][i] = in_row<M>(c, n) ? ld_stream(src + c * DT::size + 16 * i) : make_uint4(0u, 0u, 0u, 0u);
   }
+}
 
-  if (a.pre.kind) apply_norm<NV, VEC>(v, a.pre, K, red[2], red[3]);
-  if (a.n_out) {
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = 8 * (j * T + tid);
-      if (c < K) store8<VEC>(a.n_out, a.ndt, row * K + c, K - c, v[j]);
+// The row in v through the call's steps. add_r(f): v[j] = f(residual's vector j, v[j]) for all j.
+template <class HT, class RT, int NV, Mode M, class AddR>
+__device__ __forceinline__ void work_row(const RowArgs& a, const Reducer& red, int64_t row,
+                                         int64_t off, int n, float (&v)[NV][8], AddR add_r,
+                                         float* ex) {
+  constexpr bool kHasR = !std::is_same<RT, None>::value;
+  if (a.post.kind) apply_norm<NV, M>(v, a.post, a.K, n, off, red, 0);
+
+  if (a.gate) {
+    const int64_t g = (int64_t)((int)row / a.gate_tokens) * a.gate_cols;
+    if (a.gate_cols > 1) {
+      combine<NV, M>(v, a.gate, a.gdt, g + off, n,
+                     [](float2 x, float2 w) { return mul2(x, w); });
+    } else {
+      scale_all<NV>(v, load_as_f32(a.gate, a.gdt, g));
     }
   }
+  if (a.branch != 1.f) scale_all<NV>(v, a.branch);
+  if constexpr (kHasR) {
+    add_r([&](float (&x)[8], const float (&w)[8]) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) put(x, i, fma2(pair(w, i), both(a.resid), pair(x, i)));
+    });
+  }
+  if (a.r_out) store_all<NV, M>(v, a.r_out, a.rdt, row * a.ldro + off, n);
+
+  if (a.pre.kind) apply_norm<NV, M>(v, a.pre, a.K, n, off, red, 2);
+  if (a.n_out) store_all<NV, M>(v, a.n_out, a.ndt, row * a.K + off, n);
   if (!a.q) return;
 
-  if (a.T.block) apply_whiten<NV, VEC>(v, a.T, K, ex);
-  // largest magnitude as bits: they order like the values, with infinity and the NaNs on top
-  uint32_t top = 0;
+  if constexpr (M != kStrided)
+    if (a.T.block) apply_whiten<NV, M>(v, a.T, n, off, ex);
+  float big = 0.f;
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[j][e]) & 0x7fffffffu);
-  top = cta_max(top, red[1]);
+    for (int e = 0; e < 8; ++e) big = max_abs(big, v[j][e]);
+  // across threads as bits: they order like the magnitudes, with infinity and the NaNs on top
+  const uint32_t top = red.max(4, __float_as_uint(big));
   const bool finite = top < 0x7f800000u;
   const float amax = __uint_as_float(top);
-  if (tid == 0) a.q_scale[row] = finite ? amax / 127.f : __uint_as_float(0x7fffffffu);
+  const float scale =
+      finite ? (a.T.block ? amax * a.T.inv_sqrt : amax) / 127.f : __uint_as_float(0x7fffffffu);
+  if (threadIdx.x == 0 && red.rank == 0) a.q_scale[row] = scale;
   // 127 v and 127 / a must neither overflow nor lose bits: rows of extreme magnitude are moved
   // by a power of two (exact for every entry that can differ from code 0)
   float shift = 1.f;
-  const int ex_bits = (int)(top >> 23);
-  if (ex_bits < 16 || ex_bits > 240)
-    shift = __uint_as_float((uint32_t)max(1, min(253, 254 - ex_bits)) << 23);
+  const int exponent = (int)(top >> 23);
+  if (exponent < 16 || exponent > 240)
+    shift = __uint_as_float((uint32_t)max(1, min(253, 254 - exponent)) << 23);
   const float as = amax * shift;
   const float inv = finite && amax > 0.f ? 127.f / as : 0.f;
-  int8_t* qrow = a.q + row * a.ldq;
+  int8_t* qrow = a.q + row * a.ldq + off;
+  const int qn = (int)(a.ldq - off);     // columns of the stored row from here on
+  auto write = [&](auto t) {
+    typedef decltype(t) VT;              // the type of `values`, None without
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int c = 8 * (j * T + tid);
-    if (c >= (int)a.ldq) continue;
-    uint32_t lo = 0, hi = 0;
-    if (inv != 0.f) {
-      if (shift != 1.f)
+    for (int j = 0; j < NV; ++j) {
+      const int c = col_of<M>(j, 0);
+      if (M != kStrided && M != kFull && c >= qn) continue;
+      uint32_t b[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[j][e] *= shift;
-      codes8(v[j], inv, as, lo, hi);
-    }
-    *reinterpret_cast<uint2*>(qrow + c) = make_uint2(lo, hi);
-    if (a.values && c < K) {
-      const float s = finite ? amax / 127.f : __uint_as_float(0x7fffffffu);
-      float o[8];
+      for (int e = 0; e < 8; ++e) b[e] = __float_as_uint(kRound);
+      if (inv != 0.f) {
+        if (shift != 1.f)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        o[e] = s * (float)(int8_t)(lo >> (8 * e));
-        o[e + 4] = s * (float)(int8_t)(hi >> (8 * e));
+          for (int e = 0; e < 8; ++e) v[j][e] *= shift;
+        codes8(v[j], inv, as, b);
       }
-      store8<VEC>(a.values, a.vdt, row * K + c, K - c, o);
+      if constexpr (M == kStrided) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (col_of<M>(j, e) < qn) qrow[col_of<M>(j, e)] = (int8_t)b[e];
+      } else {
+        *reinterpret_cast<uint2*>(qrow + c) =
+            make_uint2(low_bytes(b[0], b[1], b[2], b[3]), low_bytes(b[4], b[5], b[6], b[7]));
+      }
+      if constexpr (VT::dt >= 0) {
+        if (!in_row<M>(c, n)) continue;
+        float o[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = scale * (__uint_as_float(b[e]) - kRound);
+        store8<VT, M>(a.values, row * a.K + off, j, n, o);
+      }
     }
+  };
+  if (!a.values) write(None{});
+  else if constexpr (is_vec(M)) write(HT{});   // values have x's type
+  else with_type(a.vdt, write);
+}
+
+// RT: the residual's type, None without one (then r_out, if any, has type a.rdt)
+template <class HT, class RT, int NV, Mode M>
+__global__ void __launch_bounds__(Form<NV, !std::is_same<RT, None>::value>::kThreads,
+                                  Form<NV, !std::is_same<RT, None>::value>::kBlocks)
+    row_kernel(const __grid_constant__ RowArgs a, int ctas) {
+  extern __shared__ __align__(16) float ex[];   // whitening blocks over 256
+  __shared__ __align__(16) uint32_t slots[kReductions * 256];
+  constexpr bool kHasR = !std::is_same<RT, None>::value;
+  const int T = blockDim.x;
+  const int row = (int)(blockIdx.x / (unsigned)ctas);
+  const Reducer red{slots, ctas, (int)(blockIdx.x - row * (unsigned)ctas)};
+  // this CTA's part of the row: n columns from column off
+  const int off = red.rank * (8 * NV) * T;
+  const int n = min(a.K - off, (8 * NV) * T);
+  // all CTAs of the cluster run before one writes to another's shared memory
+  if (ctas > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  float v[NV][8];
+  if constexpr (is_vec(M)) {
+    uint4 hr[NV][HT::size / 2], rr[NV][RT::size / 2];
+    load_raw<HT, NV, M>(hr, a.h, row * a.ldh + off, n);
+    // in flight during the first norm's reductions
+    if constexpr (kHasR) load_raw<RT, NV, M>(rr, a.r, row * a.ldr + off, n);
+    if (ctas > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+#pragma unroll
+    for (int j = 0; j < NV; ++j) unpack8<HT>(hr[j][0], hr[j][HT::size / 2 - 1], v[j]);
+    work_row<HT, RT, NV, M>(a, red, row, off, n, v, [&](auto add) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        float w[8];
+        unpack8<RT>(rr[j][0], rr[j][RT::size / 2 - 1], w);
+        add(v[j], w);
+      }
+    }, ex);
+  } else {
+    with_type(a.hdt, [&](auto t) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) load_scalar<decltype(t), M>(a.h, row * a.ldh + off, j, n, v[j]);
+    });
+    if (ctas > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    work_row<HT, RT, NV, M>(a, red, row, off, n, v, [&](auto add) {
+      with_type(a.rdt, [&](auto t) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          float w[8];
+          load_scalar<decltype(t), M>(a.r, row * a.ldr + off, j, n, w);
+          add(v[j], w);
+        }
+      });
+    }, ex);
   }
 }
 
-template <class HT, class RT, bool VEC>
-cudaError_t launch_typed(const RowArgs& a, int rows, int threads, int nv, size_t smem,
-                         cudaStream_t st) {
-  if (nv == 1) row_kernel<HT, RT, 1, VEC, 1024><<<rows, threads, smem, st>>>(a);
-  else if (nv == 4) row_kernel<HT, RT, 4, VEC, 512><<<rows, threads, smem, st>>>(a);
-  else if (threads <= 512) row_kernel<HT, RT, 8, VEC, 512><<<rows, threads, smem, st>>>(a);
-  else row_kernel<HT, RT, 8, VEC, 1024><<<rows, threads, smem, st>>>(a);
-  return cudaGetLastError();
+struct Shape {
+  int nv, ctas, threads;
+  size_t smem;
+};
+
+// CTAs of one row and their threads, with nv vectors per thread
+Shape shape_of(int K, int block, int nv) {
+  Shape s;
+  const int vecs = (K + 7) / 8, most = nv == 1 ? 1024 : 256 * nv;
+  s.nv = nv;
+  s.ctas = (vecs + most - 1) / most;
+  const int part = (vecs + s.ctas - 1) / s.ctas;
+  s.threads = (std::max(1, (part + nv - 1) / nv) + 31) / 32 * 32;
+  s.smem = 0;
+  if (block > 256) {   // 8 * threads entries hold whole blocks
+    const int unit = block / 8;
+    s.threads = (s.threads + unit - 1) / unit * unit;
+    s.smem = (size_t)s.threads * 8 * sizeof(float);
+  }
+  s.ctas = (vecs + s.threads * nv - 1) / (s.threads * nv);
+  return s;
+}
+
+template <class HT, class RT, int NV, Mode M>
+cudaError_t launch_one(const RowArgs& a, int rows, const Shape& s, cudaStream_t st) {
+  if ((int64_t)rows * s.ctas > INT32_MAX) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)rows * s.ctas);
+  cfg.blockDim = dim3(s.threads);
+  cfg.dynamicSmemBytes = s.smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = s.ctas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = s.ctas > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, row_kernel<HT, RT, NV, M>, a, s.ctas);
+}
+
+template <class HT, class RT, Mode M>
+cudaError_t launch_nv(const RowArgs& a, int rows, const Shape& s, cudaStream_t st) {
+  if (s.nv == 1) return launch_one<HT, RT, 1, M>(a, rows, s, st);
+  if constexpr (M == kVec)
+    if (a.K == s.ctas * s.threads * s.nv * 8) return launch_one<HT, RT, 4, kFull>(a, rows, s, st);
+  return launch_one<HT, RT, 4, M>(a, rows, s, st);
 }
 
 template <class HT>
-cudaError_t launch_h(const RowArgs& a, int rows, int threads, int nv, size_t smem,
-                     cudaStream_t st) {
-  const int rdt = a.r || a.r_out ? a.rdt : HT::dt;
-  if (rdt == LQ_F32) return launch_typed<HT, F32, true>(a, rows, threads, nv, smem, st);
-  if (rdt == LQ_F16) return launch_typed<HT, F16, true>(a, rows, threads, nv, smem, st);
-  return launch_typed<HT, BF16, true>(a, rows, threads, nv, smem, st);
+cudaError_t launch_h(const RowArgs& a, int rows, const Shape& s, cudaStream_t st) {
+  if (!a.r) return launch_nv<HT, None, kVec>(a, rows, s, st);
+  if (a.rdt == LQ_F32) return launch_nv<HT, F32, kVec>(a, rows, s, st);
+  if (a.rdt == LQ_F16) return launch_nv<HT, F16, kVec>(a, rows, s, st);
+  return launch_nv<HT, BF16, kVec>(a, rows, s, st);
 }
 
 bool al(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
@@ -491,22 +732,22 @@ bool vectors_ok(const RowArgs& a) {
 }
 
 cudaError_t launch_rows(const RowArgs& a, int rows, cudaStream_t st) {
-  const int vecs = (a.K + 7) / 8;
-  // One vector per thread while the rows do not fill the GPU (a few CTAs per SM): the latency of
-  // a row is what counts. Else four per thread, so that a CTA is small and several rows are in
-  // flight per SM.
-  int nv = rows <= 2 * 148 && vecs <= 1024 ? 1 : vecs <= 4 * 512 ? 4 : 8;
-  int threads = std::max(32, ((vecs + nv - 1) / nv + 31) / 32 * 32);
-  size_t smem = 0;
-  if (a.q && a.T.block > 256) {   // a slab of 8 * threads entries holds whole blocks
-    const int unit = a.T.block / 8;
-    threads = (threads + unit - 1) / unit * unit;
-    smem = (size_t)threads * 8 * sizeof(float);
+  const int block = a.q ? a.T.block : 0;
+  // the wide form while about all its threads are resident at once, for rows too short to give a
+  // thread of the small form four vectors, and for Hadamard blocks wider than its CTA
+  Shape s = shape_of(a.K, block, 1);
+  if ((int64_t)rows * s.ctas * s.threads > 148 * 1280 && a.K >= 1024 && block <= 2048)
+    s = shape_of(a.K, block, 4);
+  if (!vectors_ok(a)) {
+    if (block)
+      return a.r ? launch_nv<F32, F32, kScalar>(a, rows, s, st)
+                 : launch_nv<F32, None, kScalar>(a, rows, s, st);
+    return a.r ? launch_nv<F32, F32, kStrided>(a, rows, s, st)
+               : launch_nv<F32, None, kStrided>(a, rows, s, st);
   }
-  if (!vectors_ok(a)) return launch_typed<F32, F32, false>(a, rows, threads, nv, smem, st);
-  if (a.hdt == LQ_F32) return launch_h<F32>(a, rows, threads, nv, smem, st);
-  if (a.hdt == LQ_F16) return launch_h<F16>(a, rows, threads, nv, smem, st);
-  return launch_h<BF16>(a, rows, threads, nv, smem, st);
+  if (a.hdt == LQ_F32) return launch_h<F32>(a, rows, s, st);
+  if (a.hdt == LQ_F16) return launch_h<F16>(a, rows, s, st);
+  return launch_h<BF16>(a, rows, s, st);
 }
 
 thread_local char g_err[512];
