@@ -40,7 +40,6 @@ struct Args {
   uint32_t* status;
   int64_t ld;          // bytes per row of xq and wq
   int batch, N, K, ydt;
-  int nks, tiles_t, tiles;
 };
 
 __device__ __forceinline__ void store_y(const Args& a, int64_t i, float v) {
@@ -50,9 +49,6 @@ __device__ __forceinline__ void store_y(const Args& a, int64_t i, float v) {
 }
 
 // ------------------------------------------------------------------ few tokens
-
-constexpr int kGemvWarps = 8;
-constexpr int kGemvRows = 16;
 
 __device__ __forceinline__ uint4 ld_weights(const int8_t* p) {
   uint4 v;
@@ -70,97 +66,141 @@ __device__ __forceinline__ void mma_16832(int (&c)[4], uint32_t a0, uint32_t a1,
 }
 
 // 16 bytes of a token at k; bytes from K on read as zero, whatever the padding holds
-__device__ __forceinline__ uint4 ld_token(const int8_t* row, int k, int K) {
-  uint4 v = __ldg(reinterpret_cast<const uint4*>(row + k));
-  if (k + 16 > K) {
-    uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+__device__ __forceinline__ uint4 ld_token_end(const int8_t* row, int k, int K) {
+  uint4 v = make_uint4(0u, 0u, 0u, 0u);
+  if (k >= K) return v;
+  v = __ldg(reinterpret_cast<const uint4*>(row + k));
+  uint32_t* w = reinterpret_cast<uint32_t*>(&v);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int left = K - (k + 4 * i);
-      if (left <= 0) w[i] = 0u;
-      else if (left < 4) w[i] &= (1u << (8 * left)) - 1u;
-    }
+  for (int i = 0; i < 4; ++i) {
+    const int left = K - (k + 4 * i);
+    if (left <= 0) w[i] = 0u;
+    else if (left < 4) w[i] &= (1u << (8 * left)) - 1u;
   }
   return v;
 }
 
-template <int NT, int U>
-__global__ void __launch_bounds__(kGemvWarps * 32)
-    gemv_w8_kernel(const __grid_constant__ Args a) {
-  __shared__ int part[kGemvWarps][NT][4][32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// One CTA: 16 MT weight rows x 8 NT tokens. Its warps take steps of 64 U inputs in turn, so that
+// the CTA reads a few KB of each row at a time.
+template <int MT, int NT, int U>
+__global__ void __launch_bounds__(512) gemv_w8_kernel(const __grid_constant__ Args a) {
+  extern __shared__ int part[];   // [warps][MT][NT][4][32]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int g = lane >> 2, t = lane & 3;
-  const int n0 = blockIdx.x * kGemvRows;
+  const int n0 = blockIdx.x * (16 * MT);
   // rows past N and tokens past the batch repeat the last one; their results are not stored
-  const int8_t* w0 = a.wq + (int64_t)min(n0 + g, a.N - 1) * a.ld;
-  const int8_t* w1 = a.wq + (int64_t)min(n0 + g + 8, a.N - 1) * a.ld;
+  const int8_t* w[MT][2];
   const int8_t* x[NT];
 #pragma unroll
-  for (int i = 0; i < NT; ++i) x[i] = a.xq + (int64_t)min(8 * i + g, a.batch - 1) * a.ld;
-  int c[NT][4] = {};
-  const int ld = (int)a.ld;
-  // a warp's step is U pieces of 64 bytes of each row; the warps take steps in turn
-  for (int k0 = warp * 64 * U; k0 < ld; k0 += kGemvWarps * 64 * U) {
-    uint4 u0[U], u1[U];
+  for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int s = 0; s < U; ++s) {
-      const int k = k0 + 64 * s + 16 * t;
-      u0[s] = u1[s] = make_uint4(0u, 0u, 0u, 0u);
-      if (k < ld) {
-        u0[s] = ld_weights(w0 + k);
-        u1[s] = ld_weights(w1 + k);
-      }
-    }
+    for (int h = 0; h < 2; ++h)
+      w[m][h] = a.wq + (int64_t)min(n0 + 16 * m + 8 * h + g, a.N - 1) * a.ld + 16 * t;
 #pragma unroll
-    for (int s = 0; s < U; ++s) {
-      const int k = k0 + 64 * s + 16 * t;
+  for (int i = 0; i < NT; ++i) x[i] = a.xq + (int64_t)min(8 * i + g, a.batch - 1) * a.ld + 16 * t;
+  int c[MT][NT][4] = {};
+  const int stride = warps * (64 * U);
+  int k = warp * (64 * U);
+  for (; k + 64 * U <= a.K; k += stride) {
+    uint4 u[U][MT][2];
+#pragma unroll
+    for (int s = 0; s < U; ++s)
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) u[s][m][h] = ld_weights(w[m][h] + k + 64 * s);
+#pragma unroll
+    for (int s = 0; s < U; ++s)
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (k < ld) v = ld_token(x[i], k, a.K);
-        mma_16832(c[i], u0[s].x, u1[s].x, u0[s].y, u1[s].y, v.x, v.y);
-        mma_16832(c[i], u0[s].z, u1[s].z, u0[s].w, u1[s].w, v.z, v.w);
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(x[i] + k + 64 * s));
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          mma_16832(c[m][i], u[s][m][0].x, u[s][m][1].x, u[s][m][0].y, u[s][m][1].y, v.x, v.y);
+          mma_16832(c[m][i], u[s][m][0].z, u[s][m][1].z, u[s][m][0].w, u[s][m][1].w, v.z, v.w);
+        }
+      }
+  }
+  // the warp that holds the ragged last step
+#pragma unroll 1
+  for (const int end = min(k + 64 * U, (int)a.ld); k < end; k += 64) {
+    const bool there = k + 16 * t < (int)a.ld;
+    uint4 u[MT][2];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        u[m][h] = there ? ld_weights(w[m][h] + k) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const uint4 v = ld_token_end(x[i] - 16 * t, k + 16 * t, a.K);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        mma_16832(c[m][i], u[m][0].x, u[m][1].x, u[m][0].y, u[m][1].y, v.x, v.y);
+        mma_16832(c[m][i], u[m][0].z, u[m][1].z, u[m][0].w, u[m][1].w, v.z, v.w);
       }
     }
   }
 #pragma unroll
-  for (int i = 0; i < NT; ++i)
+  for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) part[warp][i][e][lane] = c[i][e];
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) part[(((warp * MT + m) * NT + i) * 4 + e) * 32 + lane] = c[m][i][e];
   __syncthreads();
   // c0, c1: row g, tokens 2t, 2t + 1; c2, c3: row g + 8
-  for (int o = threadIdx.x; o < 16 * 8 * NT; o += kGemvWarps * 32) {
-    const int r = o & 15, tok = o >> 4;
-    const int i = tok >> 3, src = (r & 7) * 4 + ((tok & 7) >> 1), e = (r >> 3) * 2 + (tok & 1);
+  for (int o = threadIdx.x; o < 16 * MT * 8 * NT; o += blockDim.x) {
+    const int r = o % (16 * MT), tok = o / (16 * MT), n = n0 + r;
+    if (n >= a.N || tok >= a.batch) continue;
+    const int slot = (((r >> 4) * NT + (tok >> 3)) * 4 + ((r >> 3) & 1) * 2 + (tok & 1)) * 32 +
+                     (r & 7) * 4 + ((tok & 7) >> 1);
     int acc = 0;
-#pragma unroll
-    for (int w = 0; w < kGemvWarps; ++w) acc += part[w][i][e][src];
-    const int n = n0 + r;
-    if (n < a.N && tok < a.batch) {
-      const float v = (float)acc * (a.xs[tok] * a.ws[n]) + (a.bias ? a.bias[n] : 0.f);
-      store_y(a, (int64_t)tok * a.N + n, v);
-    }
+    for (int v = 0; v < warps; ++v) acc += part[v * (MT * NT * 128) + slot];
+    store_y(a, (int64_t)tok * a.N + n,
+            (float)acc * (a.xs[tok] * a.ws[n]) + (a.bias ? a.bias[n] : 0.f));
   }
+}
+
+// per_sm: the warps that an SM should hold at least half of, all resident at once
+template <int MT, int NT, int U>
+cudaError_t launch_gemv(const Args& a, int per_sm, cudaStream_t st) {
+  const int ctas = (a.N + 16 * MT - 1) / (16 * MT);
+  int warps = 16;
+  while (warps > 1 && ((int64_t)ctas * warps > 148 * per_sm || (warps / 2) * 64 * U >= a.K))
+    warps /= 2;
+  const size_t smem = (size_t)warps * MT * NT * 128 * sizeof(int);
+  static int smem_set[64];
+  const cudaError_t e = ensure_smem((const void*)gemv_w8_kernel<MT, NT, U>, smem, smem_set);
+  if (e != cudaSuccess) return e;
+  gemv_w8_kernel<MT, NT, U><<<ctas, warps * 32, smem, st>>>(a);
+  return cudaGetLastError();
 }
 
 // ------------------------------------------------------------------ tensor-core tiles
 
-constexpr int BM = 128;                     // weight rows per tile
-constexpr int BK = 128;                     // inputs per stage: one 128-byte row
+constexpr int kMmaM = 128;                  // rows of one MMA (lanes of tensor memory)
+constexpr int kMaxTokens = 256;             // columns of one MMA
+constexpr int BK = 128;                     // inputs per chunk: one 128-byte swizzle row
 constexpr int UK = 32;                      // K of one kind::i8 MMA
-constexpr int kMaxStages = 8;
-constexpr int A_BYTES = BM * BK;
+constexpr int kMaxStages = 16;
+constexpr int kMaxChunks = 8;               // chunks per stage
 constexpr int kEpiWarps = 4;
-constexpr int kTmaWarp = 4;
-constexpr int kMmaWarp = 5;
-constexpr int kThreads = 6 * 32;
+constexpr int kWeightWarp = 4;              // fetches weights
+constexpr int kTokenWarp = 5;               // fetches tokens
+constexpr int kMmaWarp = 6;
+constexpr int kThreads = 7 * 32;
+constexpr int kTmemCols = 2 * kMaxTokens;
 constexpr uint64_t kWaitNs = 2000000000ull;
 
-template <int BT>
-struct Tile {
-  static constexpr int kStageBytes = A_BYTES + BT * BK;
-  static constexpr int kStages = BT == 256 ? 4 : (BT == 128 ? 6 : kMaxStages);
-  static constexpr int kTmemCols = 2 * BT;   // a power of two >= 32
+// One call's tiles: `rows` weight rows x `tokens` tokens over all of K, in stages of `chunks`
+// 128-byte chunks. A stage in shared memory: [chunks][rows][128 B], then [chunks][tokens][128 B].
+struct Plan {
+  int rows, tokens;          // of a tile; multiples of 8 and 16, at most 128 and 256
+  int tiles_n, tiles_t, tiles;
+  int chunks, nks, stages;   // chunks per stage, stages per tile, ring slots
+  int wide;                  // K a multiple of 128: one copy brings a stage's chunks of an operand
+  int a_bytes, stage_bytes;  // the weights of a stage; all of it
+  size_t smem;
 };
 
 struct Ctl {
@@ -172,11 +212,6 @@ struct Ctl {
   uint32_t tmem_base;
   int abort;
 };
-
-template <int BT>
-constexpr size_t smem_bytes() {
-  return 1024 + (size_t)Tile<BT>::kStages * Tile<BT>::kStageBytes + sizeof(Ctl);
-}
 
 __device__ __forceinline__ uint64_t globaltimer() {
   uint64_t t;
@@ -202,21 +237,35 @@ __device__ __forceinline__ void give_up(Ctl* ctl, uint32_t* status) {
   atomicCAS(status, 0u, (uint32_t)LQ_ETIMEOUT);
 }
 
-template <int BT>
+// A place in the ring of stages and the parity of its barriers there.
+struct Slot {
+  int at = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++at == stages) {
+      at = 0;
+      parity ^= 1;
+    }
+  }
+};
+
+// An MMA always takes 128 rows of A from shared memory. A tile of fewer rows leaves the rest to
+// whatever lies behind it there (the ring ends 16 KB before the allocation does): those lanes of
+// the accumulator are never read.
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_w8_kernel(const __grid_constant__ CUtensorMap tmap_w,
-                   const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ Args a) {
-  constexpr int NSTAGE = Tile<BT>::kStages, STAGE = Tile<BT>::kStageBytes;
+                   const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ Args a,
+                   const __grid_constant__ Plan p) {
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  Ctl* ctl = reinterpret_cast<Ctl*>(smem + (size_t)NSTAGE * STAGE);
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem_raw);
+  uint8_t* ring = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw + sizeof(Ctl)) + 1023) & ~static_cast<uintptr_t>(1023));
   volatile int* abort = &ctl->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < NSTAGE; ++s) {
-      mbar_init(&ctl->full[s], 1);
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(&ctl->full[s], 2);   // the two fetching lanes
       mbar_init(&ctl->empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -227,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ctl->abort = 0;
     mbar_fence_init();
   }
-  if (warp == kMmaWarp) tmem_alloc(&ctl->tmem_base, Tile<BT>::kTmemCols);
+  if (warp == kMmaWarp) tmem_alloc(&ctl->tmem_base, kTmemCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -236,97 +285,113 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < kEpiWarps) {
     // ---------------------------------------------------------------- epilogue
     int lt = 0;
-    for (int tile = blockIdx.x; tile < a.tiles; tile += gridDim.x, ++lt) {
-      const int tt = tile % a.tiles_t, tn = tile / a.tiles_t;
+    for (int tile = blockIdx.x; tile < p.tiles; tile += gridDim.x, ++lt) {
+      const int tn = tile / p.tiles_t, tt = tile - tn * p.tiles_t;
       const int b = lt & 1;
+      const int row = warp * 32 + lane, n = tn * p.rows + row;
+      const bool ok = row < p.rows && n < a.N;
+      const float sw = ok ? a.ws[n] : 0.f;
+      const float bias = ok && a.bias ? a.bias[n] : 0.f;
+      const int t0 = tt * p.tokens, nt = min(p.tokens, a.batch - t0);
       if (!__all_sync(0xffffffffu, wait_phase(&ctl->tmem_full[b], (lt >> 1) & 1, abort, true))) {
         give_up(ctl, a.status);
         break;
       }
       tc_fence_after();
-      const int n = tn * BM + warp * 32 + lane;
-      const bool ok = n < a.N;
-      const float sw = ok ? a.ws[n] : 0.f;
-      const float bias = ok && a.bias ? a.bias[n] : 0.f;
+      if (warp * 32 < p.rows) {
 #pragma unroll 1
-      for (int c = 0; c < BT / 32; ++c) {
-        uint32_t r[32];
-        tmem_ld_32x32b_x32(tmem + ((uint32_t)(warp * 32) << 16) + (uint32_t)(b * BT + c * 32), r);
-        const int t0 = tt * BT + c * 32;
-        const float sx = t0 + lane < a.batch ? a.xs[t0 + lane] : 0.f;
-        tmem_ld_wait();
-        if (c == BT / 32 - 1) {
-          tc_fence_before();
-          mbar_arrive(&ctl->tmem_empty[b]);
-        }
+        for (int c = 0; c < nt; c += 32) {
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(
+              tmem + ((uint32_t)(warp * 32) << 16) + (uint32_t)(b * kMaxTokens + c), r);
+          const float sx = c + lane < nt ? a.xs[t0 + c + lane] : 0.f;
+          tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const float s = __shfl_sync(0xffffffffu, sx, j) * sw;
-          if (ok && t0 + j < a.batch)
-            store_y(a, (int64_t)(t0 + j) * a.N + n, (float)(int)r[j] * s + bias);
+          for (int j = 0; j < 32; ++j) {
+            const float s = __shfl_sync(0xffffffffu, sx, j) * sw;
+            if (ok && c + j < nt)
+              store_y(a, (int64_t)(t0 + c + j) * a.N + n, (float)(int)r[j] * s + bias);
+          }
         }
       }
+      tc_fence_before();
+      mbar_arrive(&ctl->tmem_empty[b]);
     }
-  } else if (warp == kTmaWarp) {
-    // ---------------------------------------------------------------- both operands by TMA
-    if (lane == 0) {
-      prefetch_tmap(&tmap_w);
-      prefetch_tmap(&tmap_x);
-      uint32_t ctr = 0;
+  } else if (warp == kWeightWarp || warp == kTokenWarp) {
+    // ---------------------------------------------------------------- operands by TMA
+    if (elect_one()) {
+      const bool weights = warp == kWeightWarp;
+      const CUtensorMap* tmap = weights ? &tmap_w : &tmap_x;
+      prefetch_tmap(tmap);
+      const int rows = weights ? p.rows : p.tokens;
+      uint8_t* base = ring + (weights ? 0 : p.a_bytes);
+      Slot slot;
+      uint32_t issued = 0;
       bool ok = true;
-      for (int tile = blockIdx.x; ok && tile < a.tiles; tile += gridDim.x) {
-        const int tt = tile % a.tiles_t, tn = tile / a.tiles_t;
-        for (int k = 0; k < a.nks; ++k, ++ctr) {
-          const int slot = ctr % NSTAGE;
-          if (!wait_phase(&ctl->empty[slot], ((ctr / NSTAGE) & 1) ^ 1, abort, true)) {
+      for (int tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x) {
+        const int tn = tile / p.tiles_t, tt = tile - tn * p.tiles_t;
+        const int row = weights ? tn * p.rows : tt * p.tokens;
+        for (int k = 0; k < p.nks; ++k, slot.next(p.stages), ++issued) {
+          if (!wait_phase(&ctl->empty[slot.at], slot.parity ^ 1, abort, true)) {
             give_up(ctl, a.status);
             ok = false;
             break;
           }
-          uint8_t* sa = smem + (size_t)slot * STAGE;
-          mbar_arrive_expect_tx(&ctl->full[slot], STAGE);
-          tma_load_2d(sa, &tmap_w, &ctl->full[slot], k * BK, tn * BM);
-          tma_load_2d(sa + A_BYTES, &tmap_x, &ctl->full[slot], k * BK, tt * BT);
+          uint64_t* full = &ctl->full[slot.at];
+          uint8_t* at = base + slot.at * p.stage_bytes;
+          mbar_arrive_expect_tx(full, p.chunks * rows * BK);
+          if (p.wide) {
+            tma_load_3d(at, tmap, full, 0, row, k * p.chunks);
+          } else {
+            for (int c = 0; c < p.chunks; ++c)
+              tma_load_3d(at + c * rows * BK, tmap, full, (k * p.chunks + c) * BK, row, 0);
+          }
         }
       }
-      const uint32_t outstanding = ctr < NSTAGE ? ctr : NSTAGE;
-      for (uint32_t i = 0; i < outstanding; ++i) {
-        const uint32_t c = ctr - 1 - i;
-        if (!wait_phase(&ctl->full[c % NSTAGE], (c / NSTAGE) & 1, abort, false))
+      // the copies still in flight land before the CTA leaves (a stage of which only the other
+      // operand was asked for never completes: after an abort, a bounded wait)
+      for (uint32_t i = min(issued, (uint32_t)p.stages); i > 0; --i) {
+        const uint32_t c = issued - i;
+        if (!wait_phase(&ctl->full[c % p.stages], (c / p.stages) & 1, abort, false))
           give_up(ctl, a.status);
       }
     }
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- MMA issue
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_i8_s32(BM, BT);
-      uint32_t ctr = 0;
+    if (elect_one()) {
+      const uint32_t idesc = idesc_i8_s32(kMmaM, p.tokens);
+      Slot slot;
       bool ok = true;
       int lt = 0;
-      for (int tile = blockIdx.x; ok && tile < a.tiles; tile += gridDim.x, ++lt) {
+      const uint64_t desc = smem_desc_k_sw128(ring);
+      const uint32_t desc_stage = p.stage_bytes >> 4;
+      const uint32_t chunk_a = p.rows * BK >> 4, chunk_b = p.tokens * BK >> 4;
+      for (int tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x, ++lt) {
         const int b = lt & 1;
         if (!wait_phase(&ctl->tmem_empty[b], ((lt >> 1) & 1) ^ 1, abort, true)) {
           give_up(ctl, a.status);
           break;
         }
         tc_fence_after();
-        const uint32_t d = tmem + (uint32_t)(b * BT);
-        for (int k = 0; k < a.nks; ++k, ++ctr) {
-          const int slot = ctr % NSTAGE;
-          if (!wait_phase(&ctl->full[slot], (ctr / NSTAGE) & 1, abort, true)) {
+        const uint32_t d = tmem + (uint32_t)(b * kMaxTokens);
+        uint32_t more = 0;   // the tile's first MMA overwrites the accumulator
+        for (int k = 0; k < p.nks; ++k, slot.next(p.stages)) {
+          if (!wait_phase(&ctl->full[slot.at], slot.parity, abort, true)) {
             give_up(ctl, a.status);
             ok = false;
             break;
           }
           tc_fence_after();
-          uint8_t* sa = smem + (size_t)slot * STAGE;
-          const uint64_t ad = smem_desc_k_sw128(sa);
-          const uint64_t bd = smem_desc_k_sw128(sa + A_BYTES);
+          uint64_t ad = desc + (uint32_t)slot.at * desc_stage, bd = ad + (p.a_bytes >> 4);
+          for (int c = 0; c < p.chunks; ++c, ad += chunk_a, bd += chunk_b) {
 #pragma unroll
-          for (int kk = 0; kk < BK / UK; ++kk)
-            tc_mma_i8(d, ad + 2 * kk, bd + 2 * kk, idesc, (k | kk) != 0);
-          tc_commit(&ctl->empty[slot]);
+            for (int kk = 0; kk < BK / UK; ++kk) {
+              tc_mma_i8(d, ad + 2 * kk, bd + 2 * kk, idesc, more);
+              more = 1;
+            }
+          }
+          tc_commit(&ctl->empty[slot.at]);
         }
         if (ok) tc_commit(&ctl->tmem_full[b]);
       }
@@ -339,57 +404,98 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kMmaWarp) tmem_dealloc(tmem, Tile<BT>::kTmemCols);
+  if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
 // ------------------------------------------------------------------ host side
 
-// int8 rows at stride ld as a 2-D map of 128-byte x box_rows tiles; bytes from K on read as zero
-bool encode_rows(CUtensorMap* m, const int8_t* p, int64_t K, int64_t rows, int64_t ld,
-                 uint32_t box_rows) {
+constexpr size_t kMaxSmem = 227 * 1024;
+
+// The tile of a call. Rows of a tile are chosen so that its tiles fill whole waves of the SMs: few
+// rows cost nothing while the weights' stream bounds the call, and no K is split. The estimate, in
+// clocks per wave: the MMAs (8192 products per clock) against the bytes an SM takes in (about 64
+// per clock).
+Plan make_plan(int batch, int K, int N, int sms) {
+  Plan best{};
+  double best_cost = 0;
+  const int chunks_k = (K + BK - 1) / BK;
+  for (int tiles_t = (batch + kMaxTokens - 1) / kMaxTokens, tries = 0; tries < 4; ++tiles_t, ++tries) {
+    const int tokens = ((batch + tiles_t - 1) / tiles_t + 15) / 16 * 16;
+    if (tries && tokens == best.tokens) continue;
+    const int tt = (batch + tokens - 1) / tokens;
+    // the fewest waves whose tiles have at most 128 rows
+    const int64_t full = (int64_t)tt * ((N + kMmaM - 1) / kMmaM);
+    int64_t waves = (full + sms - 1) / sms;
+    int64_t tn = std::max<int64_t>(1, waves * sms / tt);
+    const int rows = std::min(kMmaM, (int)((N + tn - 1) / tn + 7) / 8 * 8);
+    tn = (N + rows - 1) / rows;
+    waves = (tn * tt + sms - 1) / sms;
+    const double mma = 4.0 * std::max(tokens, 32) / 2, load = 2.0 * (rows + tokens);
+    const double cost = (double)waves * (chunks_k * std::max(mma, load) + 1000);
+    if (best.tokens == 0 || cost < best_cost) {
+      best_cost = cost;
+      best.rows = rows;
+      best.tokens = tokens;
+      best.tiles_n = (int)tn;
+      best.tiles_t = tt;
+    }
+  }
+  best.tiles = best.tiles_n * best.tiles_t;
+  // stages of up to 48 KB, four of them at least
+  best.chunks = std::max(1, std::min({kMaxChunks, chunks_k,
+                                      48 * 1024 / ((best.rows + best.tokens) * BK)}));
+  best.wide = K % BK == 0;
+  best.a_bytes = best.chunks * best.rows * BK;
+  best.stage_bytes = best.a_bytes + best.chunks * best.tokens * BK;
+  best.nks = (chunks_k + best.chunks - 1) / best.chunks;
+  const size_t fixed = sizeof(Ctl) + 1024 + (size_t)kMmaM * BK;
+  best.stages = (int)std::min<size_t>(kMaxStages, (kMaxSmem - fixed) / best.stage_bytes);
+  best.smem = fixed + (size_t)best.stages * best.stage_bytes;
+  return best;
+}
+
+// int8 rows at stride ld as a 3-D map of boxes of box_rows x `chunks` 128-byte chunks. With K a
+// multiple of 128 the third axis counts the chunks of a row; else it has one entry, a box one
+// chunk, and the bytes from K on read as zero.
+bool encode_rows(CUtensorMap* m, const int8_t* p, int64_t K, int64_t rows, int64_t ld, int box_rows,
+                 int chunks) {
   TensorMapEncodeFn enc = tensor_map_encode_fn();
   if (enc == nullptr) return false;
-  const cuuint64_t gdim[2] = {(cuuint64_t)K, (cuuint64_t)rows};
-  const cuuint64_t gstride[1] = {(cuuint64_t)ld};
-  const cuuint32_t box[2] = {BK, box_rows};
-  const cuuint32_t estride[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(p), gdim, gstride, box,
+  const bool wide = K % BK == 0;
+  const cuuint64_t gdim[3] = {(cuuint64_t)(wide ? BK : K), (cuuint64_t)rows,
+                              (cuuint64_t)(wide ? K / BK : 1)};
+  const cuuint64_t gstride[2] = {(cuuint64_t)ld, (cuuint64_t)(wide ? BK : ld)};
+  const cuuint32_t box[3] = {BK, (cuuint32_t)box_rows, (cuuint32_t)(wide ? chunks : 1)};
+  const cuuint32_t estride[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<int8_t*>(p), gdim, gstride, box,
              estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BT>
-cudaError_t launch_tc(Args a, int sms, cudaStream_t st) {
+cudaError_t launch_tc(const Args& a, cudaStream_t st) {
+  const int sms = tc_sm_count();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  if ((int64_t)((a.N + 127) / 128) * ((a.batch + 15) / 16) > (1 << 30)) return cudaErrorInvalidValue;
+  const Plan p = make_plan(a.batch, a.K, a.N, sms);
   static int smem_set[64];
-  cudaError_t e = ensure_smem((const void*)gemm_w8_kernel<BT>, smem_bytes<BT>(), smem_set);
+  cudaError_t e = ensure_smem((const void*)gemm_w8_kernel, p.smem, smem_set);
   if (e != cudaSuccess) return e;
   CUtensorMap tw, tx;
-  if (!encode_rows(&tw, a.wq, a.K, a.N, a.ld, BM) || !encode_rows(&tx, a.xq, a.K, a.batch, a.ld, BT))
+  if (!encode_rows(&tw, a.wq, a.K, a.N, a.ld, p.rows, p.chunks) ||
+      !encode_rows(&tx, a.xq, a.K, a.batch, a.ld, p.tokens, p.chunks))
     return cudaErrorInvalidValue;
-  a.nks = (a.K + BK - 1) / BK;
-  a.tiles_t = (a.batch + BT - 1) / BT;
-  const int64_t tiles = (int64_t)a.tiles_t * ((a.N + BM - 1) / BM);
-  if (tiles > (1 << 30)) return cudaErrorInvalidValue;
-  a.tiles = (int)tiles;
-  gemm_w8_kernel<BT><<<std::min(a.tiles, sms), kThreads, smem_bytes<BT>(), st>>>(tw, tx, a);
+  gemm_w8_kernel<<<std::min(p.tiles, sms), kThreads, p.smem, st>>>(tw, tx, a, p);
   return cudaGetLastError();
 }
 
 cudaError_t launch(const Args& a, int route, cudaStream_t st) {
   if (route == LQ_I8_ROUTE_GEMV) {
-    const int grid = (a.N + kGemvRows - 1) / kGemvRows;
-    if (a.batch <= 8) gemv_w8_kernel<1, 4><<<grid, kGemvWarps * 32, 0, st>>>(a);
-    else if (a.batch <= 16) gemv_w8_kernel<2, 4><<<grid, kGemvWarps * 32, 0, st>>>(a);
-    else gemv_w8_kernel<4, 2><<<grid, kGemvWarps * 32, 0, st>>>(a);
-    return cudaGetLastError();
+    if (a.batch <= 8) return launch_gemv<1, 1, 2>(a, 50, st);
+    if (a.batch <= 16) return launch_gemv<1, 2, 4>(a, 50, st);
+    return launch_gemv<2, 4, 2>(a, 16, st);
   }
-  const int sms = tc_sm_count();
-  if (sms <= 0) return cudaErrorInvalidDevice;
-  if (a.batch <= 32) return launch_tc<32>(a, sms, st);
-  if (a.batch <= 64) return launch_tc<64>(a, sms, st);
-  if (a.batch <= 128) return launch_tc<128>(a, sms, st);
-  return launch_tc<256>(a, sms, st);
+  return launch_tc(a, st);
 }
 
 int choose(int32_t batch) {
