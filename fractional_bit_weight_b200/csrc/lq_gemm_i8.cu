@@ -10,10 +10,13 @@
 //    tokens as B (eight columns per tile). The order of k inside a sum is free, so a lane loads
 //    16 consecutive bytes of its row and of its token and feeds them as the operand words of two
 //    MMAs: no shuffles and no shared memory on the way in. One CTA takes sixteen rows, its warps
-//    interleaved over K; their int32 partials meet in shared memory.
-//  * gemm_w8_kernel (any batch): persistent tcgen05.mma kind::i8 over 128-row x BT-token tiles with
-//    two int32 accumulators in tensor memory. The weights are the 128 lanes of the accumulator, so
-//    the token tile fits the batch and a warp stores 32 consecutive outputs of a token.
+//    take turns over K; their int32 partials meet in shared memory. All warps of a call are
+//    resident at once (b1 8192 -> 28672: 41.6 us, 5.65 TB/s; three waves of CTAs took 47.6).
+//  * gemm_w8_kernel (any batch): persistent tcgen05.mma kind::i8 over tiles of up to 128 rows x 256
+//    tokens (256 x 256 by a pair of CTAs) with two int32 accumulators in tensor memory, operands
+//    brought by TMA. The weights are the lanes of the accumulator, so the token tile fits the batch
+//    and a warp stores 32 consecutive outputs of a token. Copies and MMAs are issued by an elected
+//    lane each (64 tokens x 8192 x 8192: 30 -> 20 us against a lane chosen by its number).
 // Every wait on an mbarrier is bounded in time: on expiry the kernel records LQ_ETIMEOUT in the
 // workspace status word, the roles leave their loops, in-flight copies and MMAs are waited for
 // (again bounded) and tensor memory is released before the CTA exits.
@@ -192,10 +195,12 @@ constexpr int kThreads = 7 * 32;
 constexpr int kTmemCols = 2 * kMaxTokens;
 constexpr uint64_t kWaitNs = 2000000000ull;
 
-// One call's tiles: `rows` weight rows x `tokens` tokens over all of K, in stages of `chunks`
-// 128-byte chunks. A stage in shared memory: [chunks][rows][128 B], then [chunks][tokens][128 B].
+// One call's tiles over all of K, in stages of `chunks` 128-byte chunks. A tile is `tokens` tokens
+// x `rows` weight rows per CTA (a pair of CTAs takes twice the rows, and each fetches half of the
+// tokens). A stage in shared memory: [chunks][rows][128 B], then [chunks][fetched tokens][128 B].
 struct Plan {
-  int rows, tokens;          // of a tile; multiples of 8 and 16, at most 128 and 256
+  int pair;                  // 1: CTA pairs
+  int rows, tokens;          // at most 128 and 256; multiples of 8 and of 16 (pairs: 32)
   int tiles_n, tiles_t, tiles;
   int chunks, nks, stages;   // chunks per stage, stages per tile, ring slots
   int wide;                  // K a multiple of 128: one copy brings a stage's chunks of an operand
@@ -203,7 +208,7 @@ struct Plan {
   size_t smem;
 };
 
-struct Ctl {
+struct alignas(16) Ctl {
   uint64_t full[kMaxStages];
   uint64_t empty[kMaxStages];
   uint64_t tmem_full[2];
@@ -211,6 +216,7 @@ struct Ctl {
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
+  float scale[kEpiWarps][kMaxTokens];   // each epilogue warp's copy of its tile's token scales
 };
 
 __device__ __forceinline__ uint64_t globaltimer() {
@@ -249,9 +255,90 @@ struct Slot {
   }
 };
 
-// An MMA always takes 128 rows of A from shared memory. A tile of fewer rows leaves the rest to
-// whatever lies behind it there (the ring ends 16 KB before the allocation does): those lanes of
-// the accumulator are never read.
+// One output element's conversion: values of lanes l and l ^ 1 (neighbouring channels) of two
+// tokens become one 4-byte store per lane.
+template <class YT>
+__device__ __forceinline__ uint32_t pack_y(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack_y<__half>(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t pack_y<__nv_bfloat16>(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ void put_y(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put_y(__half* p, float v) { *p = __float2half_rn(v); }
+__device__ __forceinline__ void put_y(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+// 32 tokens of one warp's 32 rows: lane = output channel, r = the tokens' sums, nt of them there.
+// A token's 32 channels are neighbours in y, so the lanes of a store fall on consecutive
+// addresses; 16-bit outputs go out two channels per lane, two tokens per store (pairs).
+template <class YT>
+__device__ __forceinline__ void write_32(const uint32_t (&r)[32], YT* y, int64_t N, bool ok, int nt,
+                                         const float* sx, float sw, float bias, bool pairs) {
+  const bool odd = threadIdx.x & 1;
+  float v[32];
+#pragma unroll
+  for (int j = 0; j < 32; j += 4) {
+    const float4 s = *reinterpret_cast<const float4*>(sx + j);
+    v[j] = fmaf((float)(int)r[j], s.x * sw, bias);
+    v[j + 1] = fmaf((float)(int)r[j + 1], s.y * sw, bias);
+    v[j + 2] = fmaf((float)(int)r[j + 2], s.z * sw, bias);
+    v[j + 3] = fmaf((float)(int)r[j + 3], s.w * sw, bias);
+  }
+  if constexpr (sizeof(YT) == 2) {
+    if (pairs && nt >= 32) {
+      uint32_t* y2 = reinterpret_cast<uint32_t*>(y + (odd ? N - 1 : 0));
+#pragma unroll
+      for (int j = 0; j < 32; j += 2) {
+        const float other = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
+        if (ok) *y2 = odd ? pack_y<YT>(other, v[j + 1]) : pack_y<YT>(v[j], other);
+        y2 += N;   // two rows of y, in pairs of channels
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    if (ok && j < nt) put_y(y, v[j]);
+    y += N;
+  }
+}
+
+// One warp's 32 rows of a finished tile: columns = tokens t0 .. t0 + nt. The next 32 columns leave
+// tensor memory while the last ones are written.
+template <class YT>
+__device__ __forceinline__ void write_tile(const Args& a, uint32_t taddr, int n, bool ok, int t0,
+                                           int nt, const float* sx, float sw, float bias) {
+  const bool pairs = sizeof(YT) == 2 && a.N % 2 == 0 && reinterpret_cast<uintptr_t>(a.y) % 4 == 0;
+  YT* y = static_cast<YT*>(a.y) + (int64_t)t0 * a.N + n;
+  uint32_t r0[32], r1[32];
+  tmem_ld_32x32b_x32(taddr, r0);
+#pragma unroll 1
+  for (int c = 0; c < nt; c += 64) {
+    tmem_ld_wait();
+    if (c + 32 < nt) tmem_ld_32x32b_x32(taddr + (uint32_t)(c + 32), r1);
+    write_32<YT>(r0, y + (int64_t)c * a.N, a.N, ok, nt - c, sx + c, sw, bias, pairs);
+    if (c + 32 >= nt) break;
+    tmem_ld_wait();
+    if (c + 64 < nt) tmem_ld_32x32b_x32(taddr + (uint32_t)(c + 64), r0);
+    write_32<YT>(r1, y + (int64_t)(c + 32) * a.N, a.N, ok, nt - c - 32, sx + c + 32, sw, bias, pairs);
+  }
+}
+
+// An MMA always takes 128 rows of A from a CTA's shared memory. A tile of fewer rows leaves the
+// rest to whatever lies behind it there (the ring ends 16 KB before the allocation does): those
+// lanes of the accumulator are never read.
+//
+// PAIR: two CTAs work on one tile of twice the rows (cta_group::2). The even CTA's barriers count
+// the copies of both, its MMA thread issues for both, and commits arrive in both. Each SM then
+// reads and fills 16 KB less shared memory per 128 inputs of a 256-token tile: one CTA alone moves
+// 24 KB per MMA through it, 192 clocks against the MMA's 128.
+template <bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_w8_kernel(const __grid_constant__ CUtensorMap tmap_w,
                    const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ Args a,
@@ -262,6 +349,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       (reinterpret_cast<uintptr_t>(smem_raw + sizeof(Ctl)) + 1023) & ~static_cast<uintptr_t>(1023));
   volatile int* abort = &ctl->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kCtas = PAIR ? 2 : 1;
+  const int rank = PAIR ? (int)(blockIdx.x & 1) : 0;    // clusters are consecutive pairs
+  const int first = (int)blockIdx.x / kCtas, step = (int)gridDim.x / kCtas;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
@@ -270,52 +360,55 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&ctl->tmem_full[b], 1);
-      mbar_init(&ctl->tmem_empty[b], kEpiWarps * 32);
+      mbar_init(&ctl->tmem_empty[b], kCtas * kEpiWarps);
     }
     mbar_init(&ctl->drain, 1);
     ctl->abort = 0;
     mbar_fence_init();
   }
-  if (warp == kMmaWarp) tmem_alloc(&ctl->tmem_base, kTmemCols);
+  if (warp == kMmaWarp) {
+    if constexpr (PAIR) tmem_alloc_pair(&ctl->tmem_base, kTmemCols);
+    else tmem_alloc(&ctl->tmem_base, kTmemCols);
+  }
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync();   // both CTAs' barriers are set up
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
 
   if (warp < kEpiWarps) {
     // ---------------------------------------------------------------- epilogue
     int lt = 0;
-    for (int tile = blockIdx.x; tile < p.tiles; tile += gridDim.x, ++lt) {
+    for (int tile = first; tile < p.tiles; tile += step, ++lt) {
       const int tn = tile / p.tiles_t, tt = tile - tn * p.tiles_t;
       const int b = lt & 1;
-      const int row = warp * 32 + lane, n = tn * p.rows + row;
+      const int row = warp * 32 + lane, n = (tn * kCtas + rank) * p.rows + row;
       const bool ok = row < p.rows && n < a.N;
+      const int t0 = tt * p.tokens, nt = min(p.tokens, a.batch - t0);
+      // the scales are on their way while the tile is summed
       const float sw = ok ? a.ws[n] : 0.f;
       const float bias = ok && a.bias ? a.bias[n] : 0.f;
-      const int t0 = tt * p.tokens, nt = min(p.tokens, a.batch - t0);
+      float* sx = ctl->scale[warp];
+      __syncwarp();
+      for (int i = lane; i < p.tokens; i += 32) sx[i] = i < nt ? a.xs[t0 + i] : 0.f;
+      __syncwarp();
       if (!__all_sync(0xffffffffu, wait_phase(&ctl->tmem_full[b], (lt >> 1) & 1, abort, true))) {
         give_up(ctl, a.status);
         break;
       }
       tc_fence_after();
       if (warp * 32 < p.rows) {
-#pragma unroll 1
-        for (int c = 0; c < nt; c += 32) {
-          uint32_t r[32];
-          tmem_ld_32x32b_x32(
-              tmem + ((uint32_t)(warp * 32) << 16) + (uint32_t)(b * kMaxTokens + c), r);
-          const float sx = c + lane < nt ? a.xs[t0 + c + lane] : 0.f;
-          tmem_ld_wait();
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float s = __shfl_sync(0xffffffffu, sx, j) * sw;
-            if (ok && c + j < nt)
-              store_y(a, (int64_t)(t0 + c + j) * a.N + n, (float)(int)r[j] * s + bias);
-          }
-        }
+        const uint32_t taddr = tmem + ((uint32_t)(warp * 32) << 16) + (uint32_t)(b * kMaxTokens);
+        if (a.ydt == LQ_BF16) write_tile<__nv_bfloat16>(a, taddr, n, ok, t0, nt, sx, sw, bias);
+        else if (a.ydt == LQ_F16) write_tile<__half>(a, taddr, n, ok, t0, nt, sx, sw, bias);
+        else write_tile<float>(a, taddr, n, ok, t0, nt, sx, sw, bias);
       }
       tc_fence_before();
-      mbar_arrive(&ctl->tmem_empty[b]);
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (PAIR) mbar_arrive_cluster(cluster_addr(&ctl->tmem_empty[b], 0));
+        else mbar_arrive(&ctl->tmem_empty[b]);
+      }
     }
   } else if (warp == kWeightWarp || warp == kTokenWarp) {
     // ---------------------------------------------------------------- operands by TMA
@@ -323,51 +416,57 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool weights = warp == kWeightWarp;
       const CUtensorMap* tmap = weights ? &tmap_w : &tmap_x;
       prefetch_tmap(tmap);
-      const int rows = weights ? p.rows : p.tokens;
+      const int rows = weights ? p.rows : p.tokens / kCtas;
       uint8_t* base = ring + (weights ? 0 : p.a_bytes);
+      const uint32_t bytes = kCtas * p.chunks * rows * BK;
       Slot slot;
       uint32_t issued = 0;
       bool ok = true;
-      for (int tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x) {
+      for (int tile = first; ok && tile < p.tiles; tile += step) {
         const int tn = tile / p.tiles_t, tt = tile - tn * p.tiles_t;
-        const int row = weights ? tn * p.rows : tt * p.tokens;
+        const int row = ((weights ? tn : tt) * kCtas + rank) * rows;
         for (int k = 0; k < p.nks; ++k, slot.next(p.stages), ++issued) {
           if (!wait_phase(&ctl->empty[slot.at], slot.parity ^ 1, abort, true)) {
             give_up(ctl, a.status);
             ok = false;
             break;
           }
-          uint64_t* full = &ctl->full[slot.at];
           uint8_t* at = base + slot.at * p.stage_bytes;
-          mbar_arrive_expect_tx(full, p.chunks * rows * BK);
-          if (p.wide) {
-            tma_load_3d(at, tmap, full, 0, row, k * p.chunks);
-          } else {
-            for (int c = 0; c < p.chunks; ++c)
-              tma_load_3d(at + c * rows * BK, tmap, full, (k * p.chunks + c) * BK, row, 0);
+          if (rank == 0) mbar_arrive_expect_tx(&ctl->full[slot.at], bytes);
+          const uint32_t full = PAIR ? cluster_addr(&ctl->full[slot.at], 0) : 0u;
+          for (int c = 0; c < (p.wide ? 1 : p.chunks); ++c) {
+            const int x = p.wide ? 0 : (k * p.chunks + c) * BK, z = p.wide ? k * p.chunks : 0;
+            if constexpr (PAIR) tma_load_3d_pair(at + c * rows * BK, tmap, full, x, row, z);
+            else tma_load_3d(at + c * rows * BK, tmap, &ctl->full[slot.at], x, row, z);
           }
         }
       }
-      // the copies still in flight land before the CTA leaves (a stage of which only the other
-      // operand was asked for never completes: after an abort, a bounded wait)
-      for (uint32_t i = min(issued, (uint32_t)p.stages); i > 0; --i) {
-        const uint32_t c = issued - i;
-        if (!wait_phase(&ctl->full[c % p.stages], (c / p.stages) & 1, abort, false))
-          give_up(ctl, a.status);
+      // the copies still in flight land before the CTA leaves (a stage of which only one operand
+      // was asked for never completes: after an abort, a bounded wait)
+      if (rank == 0) {
+        for (uint32_t i = min(issued, (uint32_t)p.stages); i > 0; --i) {
+          const uint32_t c = issued - i;
+          if (!wait_phase(&ctl->full[c % p.stages], (c / p.stages) & 1, abort, false))
+            give_up(ctl, a.status);
+        }
       }
     }
     __syncwarp();
-  } else if (warp == kMmaWarp) {
+  } else if (warp == kMmaWarp && rank == 0) {
     // ---------------------------------------------------------------- MMA issue
     if (elect_one()) {
-      const uint32_t idesc = idesc_i8_s32(kMmaM, p.tokens);
+      const uint32_t idesc = idesc_i8_s32(kCtas * kMmaM, p.tokens);
+      auto commit = [](uint64_t* bar) {
+        if constexpr (PAIR) tc_commit_pair(bar);
+        else tc_commit(bar);
+      };
       Slot slot;
       bool ok = true;
       int lt = 0;
       const uint64_t desc = smem_desc_k_sw128(ring);
       const uint32_t desc_stage = p.stage_bytes >> 4;
-      const uint32_t chunk_a = p.rows * BK >> 4, chunk_b = p.tokens * BK >> 4;
-      for (int tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x, ++lt) {
+      const uint32_t chunk_a = p.rows * BK >> 4, chunk_b = p.tokens / kCtas * BK >> 4;
+      for (int tile = first; ok && tile < p.tiles; tile += step, ++lt) {
         const int b = lt & 1;
         if (!wait_phase(&ctl->tmem_empty[b], ((lt >> 1) & 1) ^ 1, abort, true)) {
           give_up(ctl, a.status);
@@ -387,15 +486,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < p.chunks; ++c, ad += chunk_a, bd += chunk_b) {
 #pragma unroll
             for (int kk = 0; kk < BK / UK; ++kk) {
-              tc_mma_i8(d, ad + 2 * kk, bd + 2 * kk, idesc, more);
+              if constexpr (PAIR) tc_mma_i8_pair(d, ad + 2 * kk, bd + 2 * kk, idesc, more);
+              else tc_mma_i8(d, ad + 2 * kk, bd + 2 * kk, idesc, more);
               more = 1;
             }
           }
-          tc_commit(&ctl->empty[slot.at]);
+          commit(&ctl->empty[slot.at]);
         }
-        if (ok) tc_commit(&ctl->tmem_full[b]);
+        if (ok) commit(&ctl->tmem_full[b]);
       }
-      tc_commit(&ctl->drain);
+      commit(&ctl->drain);
       if (!wait_phase(&ctl->drain, 0, abort, false)) give_up(ctl, a.status);
     }
     __syncwarp();
@@ -403,8 +503,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync();   // neither CTA's memory is in use by the other any more
   tc_fence_after();
-  if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+  if (warp == kMmaWarp) {
+    if constexpr (PAIR) tmem_dealloc_pair(tmem, kTmemCols);
+    else tmem_dealloc(tmem, kTmemCols);
+  }
 }
 
 // ------------------------------------------------------------------ host side
@@ -412,41 +516,57 @@ __global__ void __launch_bounds__(kThreads, 1)
 constexpr size_t kMaxSmem = 227 * 1024;
 
 // The tile of a call. Rows of a tile are chosen so that its tiles fill whole waves of the SMs: few
-// rows cost nothing while the weights' stream bounds the call, and no K is split. The estimate, in
-// clocks per wave: the MMAs (8192 products per clock) against the bytes an SM takes in (about 64
-// per clock).
-Plan make_plan(int batch, int K, int N, int sms) {
+// rows cost nothing while the weights' stream bounds the call, and no K is split. Token tiles,
+// CTA pairs and rows are compared by an estimate in clocks, fitted to a sweep of tiles over 24 to
+// 4096 tokens and layers of 1024 x 4224 to 8192 x 28672 (the tile it picks was within 2 % of the
+// fastest on average, 9 % at worst): per 128 inputs the MMAs (2 clocks per token), the operands'
+// way into and out of shared memory (0.82 clocks per 128-byte row) or the rows fetched through L2
+// (1.67 clocks each), whichever is longest; per wave 6000; for the last epilogue 33 per token; for
+// a pair's start 4800. Pairs: 2048 x 8192 x 28672 308 against 344 us, 128 x 4096 x 4096 10.2
+// against 9.7 us.
+Plan make_plan(int batch, int K, int N, int sms, int force_pair = -1) {
   Plan best{};
   double best_cost = 0;
   const int chunks_k = (K + BK - 1) / BK;
-  for (int tiles_t = (batch + kMaxTokens - 1) / kMaxTokens, tries = 0; tries < 4; ++tiles_t, ++tries) {
-    const int tokens = ((batch + tiles_t - 1) / tiles_t + 15) / 16 * 16;
-    if (tries && tokens == best.tokens) continue;
-    const int tt = (batch + tokens - 1) / tokens;
-    // the fewest waves whose tiles have at most 128 rows
-    const int64_t full = (int64_t)tt * ((N + kMmaM - 1) / kMmaM);
-    int64_t waves = (full + sms - 1) / sms;
-    int64_t tn = std::max<int64_t>(1, waves * sms / tt);
-    const int rows = std::min(kMmaM, (int)((N + tn - 1) / tn + 7) / 8 * 8);
-    tn = (N + rows - 1) / rows;
-    waves = (tn * tt + sms - 1) / sms;
-    const double mma = 4.0 * std::max(tokens, 32) / 2, load = 2.0 * (rows + tokens);
-    const double cost = (double)waves * (chunks_k * std::max(mma, load) + 1000);
-    if (best.tokens == 0 || cost < best_cost) {
-      best_cost = cost;
-      best.rows = rows;
-      best.tokens = tokens;
-      best.tiles_n = (int)tn;
-      best.tiles_t = tt;
+  for (int pair = 0; pair < 2; ++pair) {
+    if (force_pair >= 0 && pair != force_pair) continue;
+    const int ctas = pair ? 2 : 1, units = sms / ctas, unit = 16 * ctas;
+    int last = 0;
+    for (int tiles_t = (batch + kMaxTokens - 1) / kMaxTokens, tries = 0; tries < 4; ++tiles_t, ++tries) {
+      const int tokens = ((batch + tiles_t - 1) / tiles_t + unit - 1) / unit * unit;
+      if (tokens == last) continue;
+      last = tokens;
+      const int tt = (batch + tokens - 1) / tokens;
+      // the fewest waves whose tiles have at most 128 rows per CTA
+      const int64_t full = (int64_t)tt * ((N + ctas * kMmaM - 1) / (ctas * kMmaM));
+      int64_t waves = (full + units - 1) / units;
+      int64_t tn = std::max<int64_t>(1, waves * units / tt);
+      int rows = (int)((N + ctas * tn - 1) / (ctas * tn) + 7) / 8 * 8;
+      // nearly full tiles are faster full (512 x 4096 x 4096: 13.9 against 15.4 us at 112 rows)
+      if (rows * 8 >= kMmaM * 7) rows = kMmaM;
+      tn = (N + ctas * rows - 1) / (ctas * rows);
+      waves = (tn * tt + units - 1) / units;
+      const int fetched = rows + tokens / ctas;
+      const double mma = 2.0 * tokens, smem = 0.82 * (kMmaM + tokens / ctas + fetched);
+      const double cost = pair * 4800.0 + 33.0 * tokens +
+                          (double)waves * (chunks_k * std::max({mma, smem, 1.67 * fetched}) + 6000);
+      if (best.tokens == 0 || cost < best_cost) {
+        best_cost = cost;
+        best.pair = pair;
+        best.rows = rows;
+        best.tokens = tokens;
+        best.tiles_n = (int)tn;
+        best.tiles_t = tt;
+      }
     }
   }
+  const int fetched = best.tokens / (best.pair ? 2 : 1);
   best.tiles = best.tiles_n * best.tiles_t;
   // stages of up to 48 KB, four of them at least
-  best.chunks = std::max(1, std::min({kMaxChunks, chunks_k,
-                                      48 * 1024 / ((best.rows + best.tokens) * BK)}));
+  best.chunks = std::max(1, std::min({kMaxChunks, chunks_k, 48 * 1024 / ((best.rows + fetched) * BK)}));
   best.wide = K % BK == 0;
   best.a_bytes = best.chunks * best.rows * BK;
-  best.stage_bytes = best.a_bytes + best.chunks * best.tokens * BK;
+  best.stage_bytes = best.a_bytes + best.chunks * fetched * BK;
   best.nks = (chunks_k + best.chunks - 1) / best.chunks;
   const size_t fixed = sizeof(Ctl) + 1024 + (size_t)kMmaM * BK;
   best.stages = (int)std::min<size_t>(kMaxStages, (kMaxSmem - fixed) / best.stage_bytes);
@@ -478,28 +598,45 @@ cudaError_t launch_tc(const Args& a, cudaStream_t st) {
   if (sms <= 0) return cudaErrorInvalidDevice;
   if ((int64_t)((a.N + 127) / 128) * ((a.batch + 15) / 16) > (1 << 30)) return cudaErrorInvalidValue;
   const Plan p = make_plan(a.batch, a.K, a.N, sms);
-  static int smem_set[64];
-  cudaError_t e = ensure_smem((const void*)gemm_w8_kernel, p.smem, smem_set);
+  static int smem_set[2][64];
+  const void* kernel = p.pair ? (const void*)gemm_w8_kernel<true> : (const void*)gemm_w8_kernel<false>;
+  cudaError_t e = ensure_smem(kernel, p.smem, smem_set[p.pair]);
   if (e != cudaSuccess) return e;
+  const int ctas = p.pair ? 2 : 1;
   CUtensorMap tw, tx;
   if (!encode_rows(&tw, a.wq, a.K, a.N, a.ld, p.rows, p.chunks) ||
-      !encode_rows(&tx, a.xq, a.K, a.batch, a.ld, p.tokens, p.chunks))
+      !encode_rows(&tx, a.xq, a.K, a.batch, a.ld, p.tokens / ctas, p.chunks))
     return cudaErrorInvalidValue;
-  gemm_w8_kernel<<<std::min(p.tiles, sms), kThreads, p.smem, st>>>(tw, tx, a, p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ctas * std::min(p.tiles, sms / ctas));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = p.smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.pair;
+  return p.pair ? cudaLaunchKernelEx(&cfg, gemm_w8_kernel<true>, tw, tx, a, p)
+                : cudaLaunchKernelEx(&cfg, gemm_w8_kernel<false>, tw, tx, a, p);
 }
 
 cudaError_t launch(const Args& a, int route, cudaStream_t st) {
   if (route == LQ_I8_ROUTE_GEMV) {
     if (a.batch <= 8) return launch_gemv<1, 1, 2>(a, 50, st);
-    if (a.batch <= 16) return launch_gemv<1, 2, 4>(a, 50, st);
-    return launch_gemv<2, 4, 2>(a, 16, st);
+    return launch_gemv<1, 2, 4>(a, 50, st);
   }
   return launch_tc(a, st);
 }
 
-int choose(int32_t batch) {
-  return batch <= LQ_I8_GEMV_MAX_BATCH ? LQ_I8_ROUTE_GEMV : LQ_I8_ROUTE_TC;
+// Few tokens go to the GEMV, whose start is shorter: at 8 tokens 5.2 against 10.2 us on 1024 x 8192,
+// 40.7 against 39.4 us on 28672 x 8192. Its loads of the tokens grow with the batch: at 16 tokens
+// 6.3 against 7.3 us on 4096 x 4096 and 15.5 against 15.8 on 8192 x 8192, but 47.8 against 40.1 us
+// on 28672 x 8192; at 24 tokens 19.5 against 16.0 us on 8192 x 8192.
+int choose(int32_t batch, int32_t K, int32_t N) {
+  const bool gemv = batch <= 8 || (batch <= LQ_I8_GEMV_MAX_BATCH && (int64_t)N * K <= 80 * 1000 * 1000);
+  return gemv ? LQ_I8_ROUTE_GEMV : LQ_I8_ROUTE_TC;
 }
 
 thread_local char g_err[512];
@@ -522,7 +659,7 @@ extern "C" {
 
 int32_t lq_gemm_i8_route(int32_t batch, int32_t K, int32_t N) {
   if (batch < 1 || N < 1 || K < 1 || K > LQ_MAX_I8_K) return -1;
-  return lq::w8::choose(batch);
+  return lq::w8::choose(batch, K, N);
 }
 
 lq_status lq_gemm_i8(const int8_t* xq, const float* xs, int32_t batch, const int8_t* wq,
@@ -566,7 +703,7 @@ lq_status lq_gemm_i8(const int8_t* xq, const float* xs, int32_t batch, const int
   a.N = N;
   a.K = K;
   a.ydt = ydt;
-  const cudaError_t e = launch(a, route < 0 ? choose(batch) : route, (cudaStream_t)stream);
+  const cudaError_t e = launch(a, route < 0 ? choose(batch, K, N) : route, (cudaStream_t)stream);
   return e == cudaSuccess ? LQ_OK : reject(LQ_ECUDA, "lq_gemm_i8: %s", cudaGetErrorString(e));
 }
 

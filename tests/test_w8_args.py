@@ -27,6 +27,10 @@ def test_row_bytes(L):
 def test_routes(L):
     assert lq.gemm_i8_route(1, 4096, 4096) == lq.I8_ROUTE_GEMV
     assert lq.gemm_i8_route(2048, 8192, 28672) == lq.I8_ROUTE_TC
+    assert lq.gemm_i8_route(8, 8192, 28672) == lq.I8_ROUTE_GEMV
+    assert lq.gemm_i8_route(16, 4096, 4096) == lq.I8_ROUTE_GEMV
+    assert lq.gemm_i8_route(16, 8192, 28672) == lq.I8_ROUTE_TC
+    assert lq.gemm_i8_route(17, 64, 64) == lq.I8_ROUTE_TC
     for bad in ((0, 64, 64), (1, 0, 64), (1, 64, 0), (1, 131072, 64)):
         assert lq.gemm_i8_route(*bad) == -1
 
@@ -99,7 +103,7 @@ def test_gemm_arguments(L):
         assert gemm(L, **kw) == lq.LQ_EINVAL, kw
         assert L.lq_last_error()
     assert gemm(L, K=131072) == lq.LQ_EUNSUPPORTED
-    assert gemm(L, batch=33, route=lq.I8_ROUTE_GEMV) == lq.LQ_EUNSUPPORTED
+    assert gemm(L, batch=17, route=lq.I8_ROUTE_GEMV) == lq.LQ_EUNSUPPORTED
     assert gemm(L, batch=0) == lq.LQ_OK
     assert gemm(L, N=0) == lq.LQ_OK
 
