@@ -386,7 +386,7 @@ def _rows(t, name, dtypes, device=None, shape=None):
 
 def _elsewhere(device, stream):
     """Whether a call on `device` has to leave the current device or stream."""
-    return stream is not None or device != torch.cuda.current_device()
+    return stream is not None or device != torch._C._cuda_getDevice()
 
 
 def _over_there(call, device, stream, inputs):
@@ -439,7 +439,7 @@ def quant_i8(x, sign=None, chan_scale=None, block=0, values=False, stream=None):
     rows, K = x.shape
     q = x.new_empty((rows, (K + 15) // 16 * 16), dtype=torch.int8)
     scale = x.new_empty(rows, dtype=torch.float32)
-    v = x.new_empty((rows, K)) if values else None
+    v = torch.empty_like(x, memory_format=torch.contiguous_format) if values else None
     _check(lib().lq_quant_i8(px, _DTYPES[x.dtype], rows, K, ldx,
                              _whiten_arg(sign, chan_scale, block, K, device), q.data_ptr(),
                              scale.data_ptr(), v.data_ptr() if values else None,
@@ -505,7 +505,7 @@ def _boundary(h, residual, post, pre, gate, gate_tokens, branch_scale, residual_
         pr, ldr = _rows(residual, "residual", _DTYPES, device, shape)
         rdt = _DTYPES[residual.dtype]
         if residual_out is None:
-            r_out = residual.new_empty(shape)
+            r_out = torch.empty_like(residual, memory_format=torch.contiguous_format)
             p_out = r_out.data_ptr()
         elif residual_out is residual:
             r_out, p_out = residual, pr
@@ -533,7 +533,7 @@ def _boundary(h, residual, post, pre, gate, gate_tokens, branch_scale, residual_
     if dtype is not None:
         if dtype not in _DTYPES:
             raise TypeError(f"dtype {dtype}, expected one of {tuple(_DTYPES)}")
-        n = h.new_empty(shape, dtype=dtype)
+        n = torch.empty_like(h, dtype=dtype, memory_format=torch.contiguous_format)
     _check(lib().lq_norm_residual(
         ph, _DTYPES[h.dtype], ldh, pr, rdt, ldr, rows, K, _norm_arg(post, K, device), g,
         branch_scale, residual_scale, p_out, _norm_arg(pre, K, device),

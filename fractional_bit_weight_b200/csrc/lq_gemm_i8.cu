@@ -102,6 +102,8 @@ __global__ void __launch_bounds__(512) gemv_w8_kernel(const __grid_constant__ Ar
 #pragma unroll
   for (int i = 0; i < NT; ++i) x[i] = a.xq + (int64_t)min(8 * i + g, a.batch - 1) * a.ld + 16 * t;
   int c[MT][NT][4] = {};
+  grid_release();
+  grid_wait();
   const int stride = warps * (64 * U);
   int k = warp * (64 * U);
   for (; k + 64 * U <= a.K; k += stride) {
@@ -175,8 +177,17 @@ cudaError_t launch_gemv(const Args& a, int per_sm, cudaStream_t st) {
   static int smem_set[64];
   const cudaError_t e = ensure_smem((const void*)gemv_w8_kernel<MT, NT, U>, smem, smem_set);
   if (e != cudaSuccess) return e;
-  gemv_w8_kernel<MT, NT, U><<<ctas, warps * 32, smem, st>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(warps * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, gemv_w8_kernel<MT, NT, U>, a);
 }
 
 // ------------------------------------------------------------------ tensor-core tiles
@@ -375,6 +386,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if constexpr (PAIR) cluster_sync();   // both CTAs' barriers are set up
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
+  grid_release();
+  grid_wait();
 
   if (warp < kEpiWarps) {
     // ---------------------------------------------------------------- epilogue
@@ -612,12 +625,14 @@ cudaError_t launch_tc(const Args& a, cudaStream_t st) {
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = p.smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ctas;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = p.pair;
+  cfg.numAttrs = 1 + p.pair;
   return p.pair ? cudaLaunchKernelEx(&cfg, gemm_w8_kernel<true>, tw, tx, a, p)
                 : cudaLaunchKernelEx(&cfg, gemm_w8_kernel<false>, tw, tx, a, p);
 }

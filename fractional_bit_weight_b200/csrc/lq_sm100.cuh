@@ -25,6 +25,21 @@ __device__ __forceinline__ bool elect_one() {
   return ok != 0;
 }
 
+// ------------------------------------------------------------------ programmatic launches
+// A kernel launched with the programmatic stream serialisation attribute may start while the one
+// before it on the stream still runs, once all CTAs of that one have called grid_release (or
+// ended). What it does before grid_wait must not depend on earlier work; grid_wait returns when
+// that work is complete and visible. A kernel that releases early still holds back every kernel
+// launched without the attribute until it ends.
+
+__device__ __forceinline__ void grid_release() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+__device__ __forceinline__ void grid_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // ------------------------------------------------------------------ mbarrier
 
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
