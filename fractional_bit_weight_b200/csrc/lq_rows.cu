@@ -43,6 +43,7 @@ struct RowArgs {
   int64_t ldh, ldr, ldro, ldq;
   int hdt, rdt, ndt, vdt, gdt;
   int K, gate_cols, gate_tokens;
+  int few;                // the call's CTAs are all resident at once
   float branch, resid;
   NormArgs post, pre;
   Whiten T;
@@ -626,8 +627,8 @@ __global__ void __launch_bounds__(Form<NV, !std::is_same<RT, None>::value>::kThr
   // all CTAs of the cluster run before one writes to another's shared memory
   if (ctas > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   // a few rows overlap their start with the kernel before and after (4 x 8192 codes 4.2 -> 3.7 us);
-  // many would give SMs away early (1024 x 8192 and a product behind it 75.6 -> 78.0 us)
-  if constexpr (NV == 1) {
+  // many would give SMs away early (65536 x 256 and two norms 37.4 -> 68.4 us)
+  if (NV == 1 && a.few) {
     sm100::grid_release();
     sm100::grid_wait();
   }
@@ -705,7 +706,7 @@ cudaError_t launch_one(const RowArgs& a, int rows, const Shape& s, cudaStream_t 
     attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
     ++cfg.numAttrs;
   }
-  if (NV == 1) {
+  if (NV == 1 && a.few) {
     attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
     ++cfg.numAttrs;
@@ -745,13 +746,13 @@ bool vectors_ok(const RowArgs& a) {
   return !a.q || !a.T.block || (al(a.T.sign, 8) && al(a.T.chan_scale, 16));
 }
 
-cudaError_t launch_rows(const RowArgs& a, int rows, cudaStream_t st) {
+cudaError_t launch_rows(RowArgs a, int rows, cudaStream_t st) {
   const int block = a.q ? a.T.block : 0;
   // the wide form while about all its threads are resident at once, for rows too short to give a
   // thread of the small form four vectors, and for Hadamard blocks wider than its CTA
   Shape s = shape_of(a.K, block, 1);
-  if ((int64_t)rows * s.ctas * s.threads > 148 * 1280 && a.K >= 1024 && block <= 2048)
-    s = shape_of(a.K, block, 4);
+  a.few = (int64_t)rows * s.ctas * s.threads <= 148 * 1280;
+  if (!a.few && a.K >= 1024 && block <= 2048) s = shape_of(a.K, block, 4);
   if (!vectors_ok(a)) {
     if (block)
       return a.r ? launch_nv<F32, F32, kScalar>(a, rows, s, st)
