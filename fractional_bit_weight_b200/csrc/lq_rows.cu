@@ -44,6 +44,7 @@ struct RowArgs {
   int hdt, rdt, ndt, vdt, gdt;
   int K, gate_cols, gate_tokens;
   int few;                // the call's CTAs are all resident at once
+  int plain;              // lq_quant_i8: codes of T(h) and nothing else
   float branch, resid;
   NormArgs post, pre;
   Whiten T;
@@ -61,7 +62,14 @@ struct BF16 {
   static constexpr int dt = LQ_BF16, size = 2;
   typedef __nv_bfloat16 type;
 };
+// In the place of a residual's type: a norm without a residual; lq_quant_i8, where nothing stands
+// between the input and T; and lq_quant_i8 of 16-bit inputs whose first butterflies the tensor
+// cores take.
 struct None { static constexpr int dt = -1, size = 2; };
+struct Plain : None {};
+struct PlainMma : None {};
+template <class RT> constexpr bool has_r() { return RT::dt >= 0; }
+template <class RT> constexpr bool is_plain() { return std::is_base_of<None, RT>::value && !std::is_same<RT, None>::value; }
 
 // f with the type that dt names. Loops over a thread's entries go inside f: as a branch around a
 // whole loop the choice costs nothing, inside it the compiler evaluates every type and selects.
@@ -366,13 +374,46 @@ __device__ __forceinline__ void apply_norm(float (&v)[NV][8], const NormArgs& p,
   if (p.b) combine<NV, M>(v, p.b, p.dt, off, n, [](float2 x, float2 w) { return add2(x, w); });
 }
 
+// The butterflies from distance 8 * kFirst on.
+template <int NV, int kFirst>
+__device__ __forceinline__ void finish_whiten(float (&v)[NV][8], const Whiten& T, float* ex) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int m = kFirst; m < 32; m <<= 1) {
+    if (8 * m >= T.block) break;
+    const float2 s = both((lane & m) != 0 ? -1.f : 1.f);
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 o = make_float2(__shfl_xor_sync(0xffffffffu, v[j][2 * i], m),
+                                     __shfl_xor_sync(0xffffffffu, v[j][2 * i + 1], m));
+        put(v[j], i, fma2(pair(v[j], i), s, o));
+      }
+  }
+  // the vectors j of the CTA's threads are 8 * threads consecutive entries, a whole number of
+  // blocks
+  for (int m = 32; 8 * m < T.block; m <<= 1) {
+    const float s = (threadIdx.x & m) != 0 ? -1.f : 1.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ex[e * blockDim.x + threadIdx.x] = v[j][e];
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        v[j][e] = fmaf(v[j][e], s, ex[e * blockDim.x + (threadIdx.x ^ m)]);
+    }
+  }
+}
+
 // v = sqrt(block) T(v): sign and channel scale, then butterflies over distance 1, 2, 4 in a
 // thread's vector, 8 .. 128 across the warp's lanes, 256 and up through shared memory (ex:
 // 8 * threads floats). The codes do not see a common factor and the scale takes it later.
 template <int NV, Mode M>
 __device__ __forceinline__ void apply_whiten(float (&v)[NV][8], const Whiten& T, int n, int64_t off,
                                              float* ex) {
-  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int c = col_of<M>(j, 0);
@@ -423,34 +464,63 @@ __device__ __forceinline__ void apply_whiten(float (&v)[NV][8], const Whiten& T,
             put(v[j], i + h, fma2(y, minus, x));
           }
   }
+  finish_whiten<NV, 1>(v, T, ex);
+}
+
+// T's signs and its butterflies over distance 1, 2, 8 and 16 of 16-bit inputs, as a product: with
+// the eight entries of lane (g, t) as rows g (entries 0 .. 3) and g + 8 (4 .. 7) of a 16 x 16
+// matrix, columns t and the entry's low two bits, each row times the Hadamard matrix of order 16.
+// Its columns are ordered so that every sum lands where its entry came from. The products are
+// exact and summed in fp32.
+template <class HT, int NV, Mode M>
+__device__ __forceinline__ void whiten_mma(float (&v)[NV][8], const uint4 (&raw)[NV][1],
+                                           const Whiten& T, int n, int64_t off, float* ex) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  constexpr uint32_t kOne = HT::dt == LQ_BF16 ? 0x3f803f80u : 0x3c003c00u;
+  uint32_t h[2][2];   // [output bit 1][input bit 1]: entries of input bit 0 = 0, 1
 #pragma unroll
-  for (int m = 1; m < 32; m <<= 1) {
-    if (8 * m >= T.block) break;
-    const float2 s = both((lane & m) != 0 ? -1.f : 1.f);
+  for (int j = 0; j < 2; ++j)
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+    for (int q = 0; q < 2; ++q) {
+      const uint32_t base = (uint32_t)(__popc(t & (g >> 1)) + (j & q)) & 1u;
+      h[j][q] = kOne ^ (base << 15) ^ ((base ^ (uint32_t)(g & 1)) << 31);
+    }
+  const float2 minus = both(-1.f);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 o = make_float2(__shfl_xor_sync(0xffffffffu, v[j][2 * i], m),
-                                     __shfl_xor_sync(0xffffffffu, v[j][2 * i + 1], m));
-        put(v[j], i, fma2(pair(v[j], i), s, o));
-      }
-  }
-  // the vectors j of the CTA's threads are 8 * threads consecutive entries, a whole number of
-  // blocks
-  for (int m = 32; 8 * m < T.block; m <<= 1) {
-    const float s = (threadIdx.x & m) != 0 ? -1.f : 1.f;
+  for (int j = 0; j < NV; ++j) {
+    const int c = col_of<M>(j, 0);
+    uint32_t w[4] = {raw[j][0].x, raw[j][0].y, raw[j][0].z, raw[j][0].w};
+    if (T.sign && in_row<M>(c, n)) {
+      const uint2 s = __ldg(reinterpret_cast<const uint2*>(T.sign + off + c));
+      // the sign bits of bytes 0, 1 and of 2, 3 over those of a pair of entries
+      w[0] ^= __byte_perm(s.x, 0u, 0x1404) & 0x80008000u;
+      w[1] ^= __byte_perm(s.x, 0u, 0x3424) & 0x80008000u;
+      w[2] ^= __byte_perm(s.y, 0u, 0x1404) & 0x80008000u;
+      w[3] ^= __byte_perm(s.y, 0u, 0x3424) & 0x80008000u;
+    }
+    float o[2][4];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      __syncthreads();
+    for (int k = 0; k < 2; ++k) {
+      if constexpr (HT::dt == LQ_BF16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+            "{%8,%9}, {%10,%10,%10,%10};"
+            : "=f"(o[k][0]), "=f"(o[k][1]), "=f"(o[k][2]), "=f"(o[k][3])
+            : "r"(w[0]), "r"(w[2]), "r"(w[1]), "r"(w[3]), "r"(h[k][0]), "r"(h[k][1]), "f"(0.f));
+      else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+            "{%8,%9}, {%10,%10,%10,%10};"
+            : "=f"(o[k][0]), "=f"(o[k][1]), "=f"(o[k][2]), "=f"(o[k][3])
+            : "r"(w[0]), "r"(w[2]), "r"(w[1]), "r"(w[3]), "r"(h[k][0]), "r"(h[k][1]), "f"(0.f));
+    }
+    // distance 4: entries 0 .. 3 against 4 .. 7
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ex[e * blockDim.x + threadIdx.x] = v[j][e];
-      __syncthreads();
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        v[j][e] = fmaf(v[j][e], s, ex[e * blockDim.x + (threadIdx.x ^ m)]);
+    for (int k = 0; k < 2; ++k) {
+      const float2 x = make_float2(o[k][0], o[k][1]), y = make_float2(o[k][2], o[k][3]);
+      put(v[j], k, add2(x, y));
+      put(v[j], k + 2, fma2(y, minus, x));
     }
   }
+  finish_whiten<NV, 4>(v, T, ex);
 }
 
 // Exact rounding of 127 u / a for u >= 0 next to a border m + 1/2 (m = floor): the sign of
@@ -519,38 +589,10 @@ __device__ __forceinline__ void load_raw(uint4 (&raw)[NV][DT::size / 2], const v
   }
 }
 
-// The row in v through the call's steps. add_r(f): v[j] = f(residual's vector j, v[j]) for all j.
-template <class HT, class RT, int NV, Mode M, class AddR>
-__device__ __forceinline__ void work_row(const RowArgs& a, const Reducer& red, int64_t row,
-                                         int64_t off, int n, float (&v)[NV][8], AddR add_r,
-                                         float* ex) {
-  constexpr bool kHasR = !std::is_same<RT, None>::value;
-  if (a.post.kind) apply_norm<NV, M>(v, a.post, a.K, n, off, red, 0);
-
-  if (a.gate) {
-    const int64_t g = (int64_t)((int)row / a.gate_tokens) * a.gate_cols;
-    if (a.gate_cols > 1) {
-      combine<NV, M>(v, a.gate, a.gdt, g + off, n,
-                     [](float2 x, float2 w) { return mul2(x, w); });
-    } else {
-      scale_all<NV>(v, load_as_f32(a.gate, a.gdt, g));
-    }
-  }
-  if (a.branch != 1.f) scale_all<NV>(v, a.branch);
-  if constexpr (kHasR) {
-    add_r([&](float (&x)[8], const float (&w)[8]) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) put(x, i, fma2(pair(w, i), both(a.resid), pair(x, i)));
-    });
-  }
-  if (a.r_out) store_all<NV, M>(v, a.r_out, a.rdt, row * a.ldro + off, n);
-
-  if (a.pre.kind) apply_norm<NV, M>(v, a.pre, a.K, n, off, red, 2);
-  if (a.n_out) store_all<NV, M>(v, a.n_out, a.ndt, row * a.K + off, n);
-  if (!a.q) return;
-
-  if constexpr (M != kStrided)
-    if (a.T.block) apply_whiten<NV, M>(v, a.T, n, off, ex);
+// The scale of the whitened row in v, its codes, and the values they stand for.
+template <class HT, int NV, Mode M>
+__device__ __forceinline__ void write_codes(const RowArgs& a, const Reducer& red, int64_t row,
+                                            int64_t off, int n, float (&v)[NV][8]) {
   float big = 0.f;
 #pragma unroll
   for (int j = 0; j < NV; ++j)
@@ -600,7 +642,9 @@ __device__ __forceinline__ void work_row(const RowArgs& a, const Reducer& red, i
         if (!in_row<M>(c, n)) continue;
         float o[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = scale * (__uint_as_float(b[e]) - kRound);
+        for (int i = 0; i < 4; ++i)
+          put(o, i, mul2(add2(make_float2(__uint_as_float(b[2 * i]), __uint_as_float(b[2 * i + 1])),
+                              both(-kRound)), both(scale)));
         store8<VT, M>(a.values, row * a.K + off, j, n, o);
       }
     }
@@ -610,14 +654,48 @@ __device__ __forceinline__ void work_row(const RowArgs& a, const Reducer& red, i
   else with_type(a.vdt, write);
 }
 
+// The row in v through the call's steps. add_r(f): v[j] = f(residual's vector j, v[j]) for all j.
+template <class HT, class RT, int NV, Mode M, class AddR>
+__device__ __forceinline__ void work_row(const RowArgs& a, const Reducer& red, int64_t row,
+                                         int64_t off, int n, float (&v)[NV][8], AddR add_r,
+                                         float* ex) {
+  constexpr bool kHasR = has_r<RT>();
+  if (a.post.kind) apply_norm<NV, M>(v, a.post, a.K, n, off, red, 0);
+
+  if (a.gate) {
+    const int64_t g = (int64_t)((int)row / a.gate_tokens) * a.gate_cols;
+    if (a.gate_cols > 1) {
+      combine<NV, M>(v, a.gate, a.gdt, g + off, n,
+                     [](float2 x, float2 w) { return mul2(x, w); });
+    } else {
+      scale_all<NV>(v, load_as_f32(a.gate, a.gdt, g));
+    }
+  }
+  if (a.branch != 1.f) scale_all<NV>(v, a.branch);
+  if constexpr (kHasR) {
+    add_r([&](float (&x)[8], const float (&w)[8]) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) put(x, i, fma2(pair(w, i), both(a.resid), pair(x, i)));
+    });
+  }
+  if (a.r_out) store_all<NV, M>(v, a.r_out, a.rdt, row * a.ldro + off, n);
+
+  if (a.pre.kind) apply_norm<NV, M>(v, a.pre, a.K, n, off, red, 2);
+  if (a.n_out) store_all<NV, M>(v, a.n_out, a.ndt, row * a.K + off, n);
+  if (!a.q) return;
+
+  if constexpr (M != kStrided)
+    if (a.T.block) apply_whiten<NV, M>(v, a.T, n, off, ex);
+  write_codes<HT, NV, M>(a, red, row, off, n, v);
+}
+
 // RT: the residual's type, None without one (then r_out, if any, has type a.rdt)
 template <class HT, class RT, int NV, Mode M>
-__global__ void __launch_bounds__(Form<NV, !std::is_same<RT, None>::value>::kThreads,
-                                  Form<NV, !std::is_same<RT, None>::value>::kBlocks)
+__global__ void __launch_bounds__(Form<NV, has_r<RT>()>::kThreads, Form<NV, has_r<RT>()>::kBlocks)
     row_kernel(const __grid_constant__ RowArgs a, int ctas) {
   extern __shared__ __align__(16) float ex[];   // whitening blocks over 256
   __shared__ __align__(16) uint32_t slots[kReductions * 256];
-  constexpr bool kHasR = !std::is_same<RT, None>::value;
+  constexpr bool kHasR = has_r<RT>();
   const int T = blockDim.x;
   const int row = (int)(blockIdx.x / (unsigned)ctas);
   const Reducer red{slots, ctas, (int)(blockIdx.x - row * (unsigned)ctas)};
@@ -639,8 +717,18 @@ __global__ void __launch_bounds__(Form<NV, !std::is_same<RT, None>::value>::kThr
     // in flight during the first norm's reductions
     if constexpr (kHasR) load_raw<RT, NV, M>(rr, a.r, row * a.ldr + off, n);
     if (ctas > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    if constexpr (std::is_same<RT, PlainMma>::value) {
+      whiten_mma<HT, NV, M>(v, hr, a.T, n, off, ex);
+      write_codes<HT, NV, M>(a, red, row, off, n, v);
+      return;
+    }
 #pragma unroll
     for (int j = 0; j < NV; ++j) unpack8<HT>(hr[j][0], hr[j][HT::size / 2 - 1], v[j]);
+    if constexpr (is_plain<RT>()) {
+      if (a.T.block) apply_whiten<NV, M>(v, a.T, n, off, ex);
+      write_codes<HT, NV, M>(a, red, row, off, n, v);
+      return;
+    }
     work_row<HT, RT, NV, M>(a, red, row, off, n, v, [&](auto add) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
@@ -725,6 +813,10 @@ cudaError_t launch_nv(const RowArgs& a, int rows, const Shape& s, cudaStream_t s
 
 template <class HT>
 cudaError_t launch_h(const RowArgs& a, int rows, const Shape& s, cudaStream_t st) {
+  if constexpr (HT::size == 2)
+    if (a.plain && a.T.block >= 32 && !a.T.chan_scale)
+      return launch_nv<HT, PlainMma, kVec>(a, rows, s, st);
+  if (a.plain) return launch_nv<HT, Plain, kVec>(a, rows, s, st);
   if (!a.r) return launch_nv<HT, None, kVec>(a, rows, s, st);
   if (a.rdt == LQ_F32) return launch_nv<HT, F32, kVec>(a, rows, s, st);
   if (a.rdt == LQ_F16) return launch_nv<HT, F16, kVec>(a, rows, s, st);
@@ -834,6 +926,7 @@ lq_status lq_quant_i8(const void* x, lq_dtype xdt, int32_t rows, int32_t K, int6
   a.ldh = ldx;
   a.K = K;
   a.branch = 1.f;
+  a.plain = 1;
   a.q = q;
   a.q_scale = scale;
   a.values = values;
