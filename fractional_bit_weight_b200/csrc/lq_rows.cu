@@ -6,9 +6,9 @@
 // takes a row of up to 8192 entries, a cluster of up to eight CTAs a longer one; a reduction is
 // warp shuffles and one exchange through the (cluster's) shared memory.
 //
-// A thread holds NV vectors of eight consecutive entries, vector j of thread i at column
-// 8 * (j * threads + i) of the CTA's part: a warp's 32 vectors are 256 consecutive entries, so a
-// Hadamard block of up to 256 inputs runs in one warp's registers and shuffles.
+// A thread holds NV vectors of eight consecutive entries; vectors j of a warp's threads are 256
+// consecutive entries, its NV runs follow each other. So a Hadamard block of up to 256 NV inputs
+// runs in one warp's registers and shuffles.
 //
 // What bounds it: HBM for many rows (bytes per entry: h + r + r_out + n or the codes), the latency
 // of load -> reductions -> store for a few.
@@ -43,6 +43,7 @@ struct RowArgs {
   int64_t ldh, ldr, ldro, ldq;
   int hdt, rdt, ndt, vdt, gdt;
   int K, gate_cols, gate_tokens;
+  int rows, ahead;        // the row whose inputs a CTA asks for while it works on its own
   int few;                // the call's CTAs are all resident at once
   int plain;              // lq_quant_i8: codes of T(h) and nothing else
   float branch, resid;
@@ -182,46 +183,46 @@ __host__ __device__ constexpr bool is_vec(Mode m) { return m == kVec || m == kFu
 template <Mode M>
 __device__ __forceinline__ bool in_row(int c, int n) { return M == kFull || c < n; }
 
-// column of entry e of vector j of this thread, within the CTA's part of the row
-template <Mode M>
+// column of entry e of vector j of this thread, within the CTA's part of the row: a warp's vectors
+// are NV runs of 256 entries, one behind the other
+template <int NV, Mode M>
 __device__ __forceinline__ int col_of(int j, int e) {
-  const int base = 8 * (j * (int)blockDim.x);
-  if (M == kStrided) return base + 8 * (int)(threadIdx.x & ~31u) + 32 * e + (int)(threadIdx.x & 31);
-  return base + 8 * (int)threadIdx.x + e;
+  const int base = 8 * (int)(threadIdx.x & ~31u) * NV + 256 * j, lane = threadIdx.x & 31;
+  return M == kStrided ? base + 32 * e + lane : base + 8 * lane + e;
 }
 
 // v = entries of vector j of the row part at element `off` of p, zero from column n on
-template <class DT, Mode M>
+template <class DT, int NV, Mode M>
 __device__ __forceinline__ void load_scalar(const void* p, int64_t off, int j, int n,
                                             float (&v)[8]) {
   const typename DT::type* q = static_cast<const typename DT::type*>(p) + off;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const int c = col_of<M>(j, e);
+    const int c = col_of<NV, M>(j, e);
     v[e] = c < n ? to_f32(q[c]) : 0.f;
   }
 }
 
 // the same for a vector that every row reads (a norm's weight, a gate); L1 keeps it
-template <class DT, Mode M>
+template <class DT, int NV, Mode M>
 __device__ __forceinline__ void load_shared8(const void* p, int64_t off, int j, int n,
                                              float (&v)[8]) {
   if constexpr (is_vec(M)) {
     const uint4* s = reinterpret_cast<const uint4*>(static_cast<const typename DT::type*>(p) + off +
-                                                    col_of<M>(j, 0));
+                                                    col_of<NV, M>(j, 0));
     const uint4 a = __ldg(s);
     unpack8<DT>(a, DT::size == 4 ? __ldg(s + 1) : a, v);
   } else {
-    load_scalar<DT, M>(p, off, j, n, v);
+    load_scalar<DT, NV, M>(p, off, j, n, v);
   }
 }
 
 // entries of vector j of an output row part at element `off` of p, each rounded once
-template <class DT, Mode M>
+template <class DT, int NV, Mode M>
 __device__ __forceinline__ void store8(void* p, int64_t off, int j, int n, const float (&v)[8]) {
   typename DT::type* q = static_cast<typename DT::type*>(p) + off;
   if constexpr (is_vec(M)) {
-    uint4* d = reinterpret_cast<uint4*>(q + col_of<M>(j, 0));
+    uint4* d = reinterpret_cast<uint4*>(q + col_of<NV, M>(j, 0));
     if constexpr (DT::size == 4) {
       d[0] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
                         __float_as_uint(v[3]));
@@ -234,7 +235,7 @@ __device__ __forceinline__ void store8(void* p, int64_t off, int j, int n, const
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      if (col_of<M>(j, e) < n) from_f32(v[e], q[col_of<M>(j, e)]);
+      if (col_of<NV, M>(j, e) < n) from_f32(v[e], q[col_of<NV, M>(j, e)]);
   }
 }
 
@@ -245,9 +246,9 @@ __device__ __forceinline__ void combine(float (&v)[NV][8], const void* p, int dt
   with_type(dt, [&](auto t) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      if (!in_row<M>(col_of<M>(j, 0), n)) continue;
+      if (!in_row<M>(col_of<NV, M>(j, 0), n)) continue;
       float w[8];
-      load_shared8<decltype(t), M>(p, off, j, n, w);
+      load_shared8<decltype(t), NV, M>(p, off, j, n, w);
 #pragma unroll
       for (int i = 0; i < 4; ++i) put(v[j], i, op(pair(v[j], i), pair(w, i)));
     }
@@ -260,7 +261,7 @@ __device__ __forceinline__ void store_all(const float (&v)[NV][8], void* p, int 
   with_type(dt, [&](auto t) {
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      if (in_row<M>(col_of<M>(j, 0), n)) store8<decltype(t), M>(p, off, j, n, v[j]);
+      if (in_row<M>(col_of<NV, M>(j, 0), n)) store8<decltype(t), NV, M>(p, off, j, n, v[j]);
   });
 }
 
@@ -357,7 +358,7 @@ __device__ __forceinline__ void apply_norm(float (&v)[NV][8], const NormArgs& p,
     for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (in_row<M>(col_of<M>(j, e), n)) v[j][e] -= mean;
+        if (in_row<M>(col_of<NV, M>(j, e), n)) v[j][e] -= mean;
   }
   float2 ss = both(0.f);
 #pragma unroll
@@ -391,9 +392,22 @@ __device__ __forceinline__ void finish_whiten(float (&v)[NV][8], const Whiten& T
         put(v[j], i, fma2(pair(v[j], i), s, o));
       }
   }
-  // the vectors j of the CTA's threads are 8 * threads consecutive entries, a whole number of
-  // blocks
-  for (int m = 32; 8 * m < T.block; m <<= 1) {
+  // distance 256 and 512 between a thread's own vectors
+#pragma unroll
+  for (int h = 1; h < NV; h <<= 1)
+    if (256 * h < T.block) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if ((j & h) == 0)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 x = pair(v[j], i), y = pair(v[j + h], i);
+            put(v[j], i, add2(x, y));
+            put(v[j + h], i, fma2(y, both(-1.f), x));
+          }
+    }
+  // the rest between warps; a CTA's part is a whole number of blocks
+  for (int m = 32; 8 * NV * m < T.block; m <<= 1) {
     const float s = (threadIdx.x & m) != 0 ? -1.f : 1.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -409,18 +423,18 @@ __device__ __forceinline__ void finish_whiten(float (&v)[NV][8], const Whiten& T
 }
 
 // v = sqrt(block) T(v): sign and channel scale, then butterflies over distance 1, 2, 4 in a
-// thread's vector, 8 .. 128 across the warp's lanes, 256 and up through shared memory (ex:
-// 8 * threads floats). The codes do not see a common factor and the scale takes it later.
+// thread's vector, 8 .. 128 across the warp's lanes, 256 and up between a thread's vectors and
+// through shared memory (ex: 8 * threads floats). The codes do not see a common factor and the scale takes it later.
 template <int NV, Mode M>
 __device__ __forceinline__ void apply_whiten(float (&v)[NV][8], const Whiten& T, int n, int64_t off,
                                              float* ex) {
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int c = col_of<M>(j, 0);
+    const int c = col_of<NV, M>(j, 0);
     if (in_row<M>(c, n)) {
       if (T.chan_scale) {
         float cs[8];
-        load_shared8<F32, M>(T.chan_scale, off, j, n, cs);
+        load_shared8<F32, NV, M>(T.chan_scale, off, j, n, cs);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[j][e] *= cs[e];
       }
@@ -488,7 +502,7 @@ __device__ __forceinline__ void whiten_mma(float (&v)[NV][8], const uint4 (&raw)
   const float2 minus = both(-1.f);
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int c = col_of<M>(j, 0);
+    const int c = col_of<NV, M>(j, 0);
     uint32_t w[4] = {raw[j][0].x, raw[j][0].y, raw[j][0].z, raw[j][0].w};
     if (T.sign && in_row<M>(c, n)) {
       const uint2 s = __ldg(reinterpret_cast<const uint2*>(T.sign + off + c));
@@ -582,7 +596,7 @@ __device__ __forceinline__ void load_raw(uint4 (&raw)[NV][DT::size / 2], const v
   const char* src = static_cast<const char*>(p) + first * DT::size;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int c = col_of<kVec>(j, 0);
+    const int c = col_of<NV, kVec>(j, 0);
 #pragma unroll
     for (int i = 0; i < DT::size / 2; ++i)
       raw[j][i] = in_row<M>(c, n) ? ld_stream(src + c * DT::size + 16 * i) : make_uint4(0u, 0u, 0u, 0u);
@@ -619,7 +633,7 @@ __device__ __forceinline__ void write_codes(const RowArgs& a, const Reducer& red
     typedef decltype(t) VT;              // the type of `values`, None without
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = col_of<M>(j, 0);
+      const int c = col_of<NV, M>(j, 0);
       if (M != kStrided && M != kFull && c >= qn) continue;
       uint32_t b[8];
 #pragma unroll
@@ -633,7 +647,7 @@ __device__ __forceinline__ void write_codes(const RowArgs& a, const Reducer& red
       if constexpr (M == kStrided) {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          if (col_of<M>(j, e) < qn) qrow[col_of<M>(j, e)] = (int8_t)b[e];
+          if (col_of<NV, M>(j, e) < qn) qrow[col_of<NV, M>(j, e)] = (int8_t)b[e];
       } else {
         *reinterpret_cast<uint2*>(qrow + c) =
             make_uint2(low_bytes(b[0], b[1], b[2], b[3]), low_bytes(b[4], b[5], b[6], b[7]));
@@ -645,13 +659,21 @@ __device__ __forceinline__ void write_codes(const RowArgs& a, const Reducer& red
         for (int i = 0; i < 4; ++i)
           put(o, i, mul2(add2(make_float2(__uint_as_float(b[2 * i]), __uint_as_float(b[2 * i + 1])),
                               both(-kRound)), both(scale)));
-        store8<VT, M>(a.values, row * a.K + off, j, n, o);
+        store8<VT, NV, M>(a.values, row * a.K + off, j, n, o);
       }
     }
   };
   if (!a.values) write(None{});
   else if constexpr (is_vec(M)) write(HT{});   // values have x's type
   else with_type(a.vdt, write);
+}
+
+// n entries of an input into L2
+template <class DT>
+__device__ __forceinline__ void prefetch_row(const void* p, int64_t first, int n) {
+  const char* src = static_cast<const char*>(p) + first * DT::size;
+  for (int b = threadIdx.x * 128; b < n * DT::size; b += blockDim.x * 128)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(src + b));
 }
 
 // The row in v through the call's steps. add_r(f): v[j] = f(residual's vector j, v[j]) for all j.
@@ -716,20 +738,21 @@ __global__ void __launch_bounds__(Form<NV, has_r<RT>()>::kThreads, Form<NV, has_
     load_raw<HT, NV, M>(hr, a.h, row * a.ldh + off, n);
     // in flight during the first norm's reductions
     if constexpr (kHasR) load_raw<RT, NV, M>(rr, a.r, row * a.ldr + off, n);
+    if (NV > 1 && row + a.ahead < a.rows) {
+      prefetch_row<HT>(a.h, (row + a.ahead) * a.ldh + off, n);
+      if constexpr (kHasR) prefetch_row<RT>(a.r, (row + a.ahead) * a.ldr + off, n);
+    }
     if (ctas > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     if constexpr (std::is_same<RT, PlainMma>::value) {
       whiten_mma<HT, NV, M>(v, hr, a.T, n, off, ex);
-      write_codes<HT, NV, M>(a, red, row, off, n, v);
-      return;
-    }
+    } else {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) unpack8<HT>(hr[j][0], hr[j][HT::size / 2 - 1], v[j]);
-    if constexpr (is_plain<RT>()) {
-      if (a.T.block) apply_whiten<NV, M>(v, a.T, n, off, ex);
-      write_codes<HT, NV, M>(a, red, row, off, n, v);
-      return;
+      for (int j = 0; j < NV; ++j) unpack8<HT>(hr[j][0], hr[j][HT::size / 2 - 1], v[j]);
+      if constexpr (is_plain<RT>())
+        if (a.T.block) apply_whiten<NV, M>(v, a.T, n, off, ex);
     }
-    work_row<HT, RT, NV, M>(a, red, row, off, n, v, [&](auto add) {
+    if constexpr (is_plain<RT>()) write_codes<HT, NV, M>(a, red, row, off, n, v);
+    else work_row<HT, RT, NV, M>(a, red, row, off, n, v, [&](auto add) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         float w[8];
@@ -740,7 +763,7 @@ __global__ void __launch_bounds__(Form<NV, has_r<RT>()>::kThreads, Form<NV, has_
   } else {
     with_type(a.hdt, [&](auto t) {
 #pragma unroll
-      for (int j = 0; j < NV; ++j) load_scalar<decltype(t), M>(a.h, row * a.ldh + off, j, n, v[j]);
+      for (int j = 0; j < NV; ++j) load_scalar<decltype(t), NV, M>(a.h, row * a.ldh + off, j, n, v[j]);
     });
     if (ctas > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     work_row<HT, RT, NV, M>(a, red, row, off, n, v, [&](auto add) {
@@ -748,7 +771,7 @@ __global__ void __launch_bounds__(Form<NV, has_r<RT>()>::kThreads, Form<NV, has_
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
           float w[8];
-          load_scalar<decltype(t), M>(a.r, row * a.ldr + off, j, n, w);
+          load_scalar<decltype(t), NV, M>(a.r, row * a.ldr + off, j, n, w);
           add(v[j], w);
         }
       });
@@ -770,10 +793,10 @@ Shape shape_of(int K, int block, int nv) {
   const int part = (vecs + s.ctas - 1) / s.ctas;
   s.threads = (std::max(1, (part + nv - 1) / nv) + 31) / 32 * 32;
   s.smem = 0;
-  if (block > 256) {   // 8 * threads entries hold whole blocks
-    const int unit = block / 8;
+  if (block > 256) {   // a CTA's part holds whole blocks
+    const int unit = std::max(32, block / (8 * nv));
     s.threads = (s.threads + unit - 1) / unit * unit;
-    s.smem = (size_t)s.threads * 8 * sizeof(float);
+    if (block > 256 * nv) s.smem = (size_t)s.threads * 8 * sizeof(float);
   }
   s.ctas = (vecs + s.threads * nv - 1) / (s.threads * nv);
   return s;
@@ -840,11 +863,14 @@ bool vectors_ok(const RowArgs& a) {
 
 cudaError_t launch_rows(RowArgs a, int rows, cudaStream_t st) {
   const int block = a.q ? a.T.block : 0;
-  // the wide form while about all its threads are resident at once, for rows too short to give a
-  // thread of the small form four vectors, and for Hadamard blocks wider than its CTA
+  // the wide form while about all its threads are resident at once, and for rows too short to give
+  // a thread of the small form four vectors
   Shape s = shape_of(a.K, block, 1);
+  // Half as many rows ahead as are in flight (2048 x 28672 codes 85 -> 76 us, 2048 x 8192 boundary
+  // 34.2 -> 31.9); a whole wave ahead or two were slower (32.5, 35.5).
+  a.ahead = std::max(1, 148 * (a.r ? 3 : 4) * 256 / 2 / std::max(1, (a.K + 31) / 32));
   a.few = (int64_t)rows * s.ctas * s.threads <= 148 * 1280;
-  if (!a.few && a.K >= 1024 && block <= 2048) s = shape_of(a.K, block, 4);
+  if (!a.few && a.K >= 1024) s = shape_of(a.K, block, 4);
   if (!vectors_ok(a)) {
     if (block)
       return a.r ? launch_nv<F32, F32, kScalar>(a, rows, s, st)
@@ -921,6 +947,7 @@ lq_status lq_quant_i8(const void* x, lq_dtype xdt, int32_t rows, int32_t K, int6
   RowArgs a{};
   st = lq::whiten_from_desc(T, K, &a.T);
   if (st != LQ_OK) return st;
+  a.rows = rows;
   a.h = x;
   a.hdt = a.vdt = xdt;
   a.ldh = ldx;
@@ -968,6 +995,7 @@ lq_status lq_norm_residual(const void* h, lq_dtype hdt, int64_t ldh, const void*
       (n_out && !al(n_out, width(ndt))) || !al(q, 16) || !al(q_scale, 4) ||
       (gate && !al(gate->gate, width(gate->dtype))))
     return reject(LQ_EINVAL, "%s: misaligned pointer", me);
+  a.rows = rows;
   a.h = h;
   a.hdt = hdt;
   a.ldh = ldh;
