@@ -527,6 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ------------------------------------------------------------------ host side
 
 constexpr size_t kMaxSmem = 227 * 1024;
+constexpr int32_t kMost = 1 << 30;          // tokens, rows: tile coordinates stay in 32 bits
 
 // The tile of a call. Rows of a tile are chosen so that its tiles fill whole waves of the SMs: few
 // rows cost nothing while the weights' stream bounds the call, and no K is split. Token tiles,
@@ -606,11 +607,11 @@ bool encode_rows(CUtensorMap* m, const int8_t* p, int64_t K, int64_t rows, int64
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-cudaError_t launch_tc(const Args& a, cudaStream_t st) {
+cudaError_t launch_tc(const Args& a, int force_pair, cudaStream_t st) {
   const int sms = tc_sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
   if ((int64_t)((a.N + 127) / 128) * ((a.batch + 15) / 16) > (1 << 30)) return cudaErrorInvalidValue;
-  const Plan p = make_plan(a.batch, a.K, a.N, sms);
+  const Plan p = make_plan(a.batch, a.K, a.N, sms, force_pair);
   static int smem_set[2][64];
   const void* kernel = p.pair ? (const void*)gemm_w8_kernel<true> : (const void*)gemm_w8_kernel<false>;
   cudaError_t e = ensure_smem(kernel, p.smem, smem_set[p.pair]);
@@ -637,21 +638,20 @@ cudaError_t launch_tc(const Args& a, cudaStream_t st) {
                 : cudaLaunchKernelEx(&cfg, gemm_w8_kernel<false>, tw, tx, a, p);
 }
 
-cudaError_t launch(const Args& a, int route, cudaStream_t st) {
-  if (route == LQ_I8_ROUTE_GEMV) {
-    if (a.batch <= 8) return launch_gemv<1, 1, 2>(a, 50, st);
-    return launch_gemv<1, 2, 4>(a, 50, st);
-  }
-  return launch_tc(a, st);
-}
-
 // Few tokens go to the GEMV, whose start is shorter: at 8 tokens 5.2 against 10.2 us on 1024 x 8192,
 // 40.7 against 39.4 us on 28672 x 8192. Its loads of the tokens grow with the batch: at 16 tokens
 // 6.3 against 7.3 us on 4096 x 4096 and 15.5 against 15.8 on 8192 x 8192, but 47.8 against 40.1 us
 // on 28672 x 8192; at 24 tokens 19.5 against 16.0 us on 8192 x 8192.
-int choose(int32_t batch, int32_t K, int32_t N) {
-  const bool gemv = batch <= 8 || (batch <= LQ_I8_GEMV_MAX_BATCH && (int64_t)N * K <= 80 * 1000 * 1000);
-  return gemv ? LQ_I8_ROUTE_GEMV : LQ_I8_ROUTE_TC;
+bool few_tokens(int32_t batch, int32_t K, int32_t N) {
+  return batch <= 8 || (batch <= LQ_I8_GEMV_MAX_BATCH && (int64_t)N * K <= 80 * 1000 * 1000);
+}
+
+cudaError_t launch(const Args& a, int route, cudaStream_t st) {
+  if (route < 0 ? few_tokens(a.batch, a.K, a.N) : route == LQ_I8_ROUTE_GEMV) {
+    if (a.batch <= 8) return launch_gemv<1, 1, 2>(a, 50, st);
+    return launch_gemv<1, 2, 4>(a, 50, st);
+  }
+  return launch_tc(a, route < 0 ? -1 : route == LQ_I8_ROUTE_PAIR, st);
 }
 
 thread_local char g_err[512];
@@ -673,8 +673,10 @@ bool al(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 
 extern "C" {
 
 int32_t lq_gemm_i8_route(int32_t batch, int32_t K, int32_t N) {
-  if (batch < 1 || N < 1 || K < 1 || K > LQ_MAX_I8_K) return -1;
-  return lq::w8::choose(batch, K, N);
+  using namespace lq::w8;
+  if (batch < 1 || N < 1 || K < 1 || K > LQ_MAX_I8_K || batch > kMost || N > kMost) return -1;
+  if (few_tokens(batch, K, N)) return LQ_I8_ROUTE_GEMV;
+  return make_plan(batch, K, N, 148).pair ? LQ_I8_ROUTE_PAIR : LQ_I8_ROUTE_TC;
 }
 
 lq_status lq_gemm_i8(const int8_t* xq, const float* xs, int32_t batch, const int8_t* wq,
@@ -688,9 +690,11 @@ lq_status lq_gemm_i8(const int8_t* xq, const float* xs, int32_t batch, const int
   if (K < 1) return reject(LQ_EINVAL, "lq_gemm_i8: K = %d < 1", K);
   if (K > LQ_MAX_I8_K)
     return reject(LQ_EUNSUPPORTED, "lq_gemm_i8: K = %d exceeds LQ_MAX_I8_K (%d)", K, LQ_MAX_I8_K);
+  if (batch > kMost || N > kMost)
+    return reject(LQ_EUNSUPPORTED, "lq_gemm_i8: batch = %d or N = %d exceeds %d", batch, N, kMost);
   if (ydt != LQ_F32 && ydt != LQ_F16 && ydt != LQ_BF16)
     return reject(LQ_EINVAL, "lq_gemm_i8: unknown y dtype %d", (int)ydt);
-  if (route < -1 || route > LQ_I8_ROUTE_TC)
+  if (route < -1 || route > LQ_I8_ROUTE_PAIR)
     return reject(LQ_EINVAL, "lq_gemm_i8: unknown route %d", route);
   if (route == LQ_I8_ROUTE_GEMV && batch > LQ_I8_GEMV_MAX_BATCH)
     return reject(LQ_EUNSUPPORTED, "lq_gemm_i8: %d tokens on the GEMV route (at most %d)", batch,
@@ -718,7 +722,7 @@ lq_status lq_gemm_i8(const int8_t* xq, const float* xs, int32_t batch, const int
   a.N = N;
   a.K = K;
   a.ydt = ydt;
-  const cudaError_t e = launch(a, route < 0 ? choose(batch, K, N) : route, (cudaStream_t)stream);
+  const cudaError_t e = launch(a, route, (cudaStream_t)stream);
   return e == cudaSuccess ? LQ_OK : reject(LQ_ECUDA, "lq_gemm_i8: %s", cudaGetErrorString(e));
 }
 

@@ -351,6 +351,7 @@ LQ_API lq_status lq_norm_residual(const void* h, lq_dtype hdt, int64_t ldh, cons
 /* Kernel routes of lq_gemm_i8. */
 #define LQ_I8_ROUTE_GEMV 0  /* warp-level int8 MMA, up to LQ_I8_GEMV_MAX_BATCH tokens */
 #define LQ_I8_ROUTE_TC 1    /* tcgen05 kind::i8 tiles, any batch */
+#define LQ_I8_ROUTE_PAIR 2  /* the same tiles by pairs of CTAs, any batch */
 #define LQ_I8_GEMV_MAX_BATCH 16
 /* Bytes of the lq_gemm_i8 workspace: the status word. */
 #define LQ_GEMM_I8_WORKSPACE_BYTES 256
@@ -370,8 +371,8 @@ LQ_API int32_t lq_gemm_i8_route(int32_t batch, int32_t K, int32_t N);
  *   first use; holds the status word that lq_device_status reads.
  *   route: -1 lets the library choose, an LQ_I8_ROUTE_* code asks for that kernel.
  * Errors: LQ_EINVAL (null or misaligned pointers, batch < 0, N < 0, K < 1, unknown dtype or
- * route, workspace too small), LQ_EUNSUPPORTED (K > LQ_MAX_I8_K, a route that does not take the
- * batch), LQ_ECUDA. batch = 0 or N = 0 is a no-op. */
+ * route, workspace too small), LQ_EUNSUPPORTED (K > LQ_MAX_I8_K, batch or N > 2^30, a route that
+ * does not take the batch), LQ_ECUDA. batch = 0 or N = 0 is a no-op. */
 LQ_API lq_status lq_gemm_i8(const int8_t* xq, const float* xs, int32_t batch, const int8_t* wq,
                             const float* ws, const float* bias, int32_t K, int32_t N, void* y,
                             lq_dtype ydt, void* workspace, size_t workspace_bytes, int32_t route,

@@ -195,6 +195,28 @@ def test_gemm_small_batches_on_both_routes(batch, K, N, route):
     check_gemm(batch, K, N, F32, True, route=route)
 
 
+@pytest.mark.parametrize("batch,K,N", [(1, 1, 1), (3, 128, 256), (17, 100, 257), (31, 8192, 8),
+                                       (33, 2048, 1000), (64, 4100, 515), (100, 128, 30),
+                                       (129, 1000, 2050), (256, 512, 512), (257, 384, 770),
+                                       (700, 640, 5001), (1025, 200, 300), (300, 2056, 19000)])
+@pytest.mark.parametrize("route", [lq.I8_ROUTE_TC, lq.I8_ROUTE_PAIR])
+def test_gemm_tile_kernels(batch, K, N, route):
+    check_gemm(batch, K, N, BF16, False, route=route)
+    check_gemm(batch, K, N, F32, True, route=route)
+
+
+@pytest.mark.parametrize("route", [lq.I8_ROUTE_TC, lq.I8_ROUTE_PAIR])
+def test_gemm_tiles_with_odd_rows_of_y(route):
+    """16-bit outputs at an odd width or off a 4-byte boundary are stored one by one."""
+    check_gemm(70, 256, 333, F16, True, route=route)
+    batch, K, N = 70, 256, 334
+    xq, wq, xs, sw = int8(batch, K, 1), int8(N, K, 2), scales(batch, 3), scales(N, 4)
+    flat = torch.zeros(batch * N + 1, dtype=BF16, device=DEV)
+    y = lq.gemm_i8(xq, xs, wq, sw, y=flat[1:].view(batch, N), route=route)
+    ref.within(y, *ref.product(xq, xs, wq, sw, K, None))
+    assert flat[0] == 0
+
+
 @pytest.mark.parametrize("batch", [3, 40, 300])
 def test_gemm_ignores_the_padding(batch):
     check_gemm(batch, 1003, 150, F32, False, fill=77)
@@ -228,6 +250,33 @@ def test_gemm_full_size_layers():
         check_gemm(batch, K, N, BF16, False)
 
 
+def test_offsets_past_32_bits():
+    """Rows whose elements lie beyond 2^31 equal the same rows on their own."""
+    rows, K = 270000, 8192
+    x = torch.empty(rows, K, dtype=BF16, device=DEV)
+    x[:] = rand(1000, K, BF16, 1).repeat(rows // 1000, 1)
+    x[-1] = rand(1, K, BF16, 2)
+    q, s = lq.quant_i8(x, block=256)
+    for at in (0, rows // 2, rows - 3):
+        q2, s2 = lq.quant_i8(x[at:at + 3].clone(), block=256)
+        assert torch.equal(q[at:at + 3], q2) and torch.equal(s[at:at + 3], s2)
+    del q, s
+    pre = lq.Norm("rms")
+    c, n = lq.norm_residual(x, x, None, pre)
+    c2, n2 = lq.norm_residual(x[-3:].clone(), x[-3:].clone(), None, pre)
+    # the two calls split a row over threads differently: one rounding step of bf16 apart at most
+    assert torch.equal(c[-3:], c2)
+    assert ((n[-3:].float() - n2.float()).abs() <= 2.0 ** -7 * n2.float().abs()).all()
+    del x, c, n
+    batch, K, N = 70000, 64, 32768
+    xq, wq, xs, sw = int8(batch, K, 1), int8(N, K, 2), scales(batch, 3), scales(N, 4)
+    for route in (lq.I8_ROUTE_TC, lq.I8_ROUTE_PAIR):
+        y = lq.gemm_i8(xq, xs, wq, sw, dtype=BF16, route=route)
+        ref.within(y[-5:], *ref.product(xq[-5:], xs[-5:], wq, sw, K, None))
+        ref.within(y[:5], *ref.product(xq[:5], xs[:5], wq, sw, K, None))
+        del y
+
+
 def test_gemm_empty():
     wq, sw = int8(10, 64, 1), scales(10, 1)
     y = lq.gemm_i8(int8(0, 64, 1), scales(0, 1), wq, sw)
@@ -245,6 +294,7 @@ def test_gemm_same_bits_every_time():
         assert torch.equal(y, lq.gemm_i8(xq, xs, wq, sw))
         if batch <= 16:     # the integer sum does not depend on the kernel
             assert torch.equal(y, lq.gemm_i8(xq, xs, wq, sw, route=lq.I8_ROUTE_TC))
+        assert torch.equal(y, lq.gemm_i8(xq, xs, wq, sw, route=lq.I8_ROUTE_PAIR))
 
 
 def test_graphs_share_a_workspace():
