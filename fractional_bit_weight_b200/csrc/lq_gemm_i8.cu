@@ -166,12 +166,14 @@ __global__ void __launch_bounds__(512) gemv_w8_kernel(const __grid_constant__ Ar
   }
 }
 
-// per_sm: the warps that an SM should hold at least half of, all resident at once
 template <int MT, int NT, int U>
-cudaError_t launch_gemv(const Args& a, int per_sm, cudaStream_t st) {
+cudaError_t launch_gemv(const Args& a, cudaStream_t st) {
   const int ctas = (a.N + 16 * MT - 1) / (16 * MT);
+  // Up to 31 warps per SM, which registers let be resident at once, but four to a CTA at least, and
+  // some steps for each. One token x 8192 x 10240: 18.0 us with four warps (17 per SM), 19.2 with
+  // eight (35); 8192 x 28672: 41.0 with four (48), 42.4 with two (24).
   int warps = 16;
-  while (warps > 1 && ((int64_t)ctas * warps > 148 * per_sm || (warps / 2) * 64 * U >= a.K))
+  while ((warps > 4 && (int64_t)ctas * warps > 148 * 31) || (warps > 1 && (warps / 2) * 64 * U >= a.K))
     warps /= 2;
   const size_t smem = (size_t)warps * MT * NT * 128 * sizeof(int);
   static int smem_set[64];
@@ -648,8 +650,8 @@ bool few_tokens(int32_t batch, int32_t K, int32_t N) {
 
 cudaError_t launch(const Args& a, int route, cudaStream_t st) {
   if (route < 0 ? few_tokens(a.batch, a.K, a.N) : route == LQ_I8_ROUTE_GEMV) {
-    if (a.batch <= 8) return launch_gemv<1, 1, 2>(a, 50, st);
-    return launch_gemv<1, 2, 4>(a, 50, st);
+    if (a.batch <= 8) return launch_gemv<1, 1, 2>(a, st);
+    return launch_gemv<1, 2, 4>(a, st);
   }
   return launch_tc(a, route < 0 ? -1 : route == LQ_I8_ROUTE_PAIR, st);
 }
