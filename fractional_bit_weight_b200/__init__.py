@@ -350,43 +350,48 @@ _NORM_KINDS = {"rms": 1, "layer": 2}
 
 def _arg(t, name, dtypes, device, shape=None):
     """The address of a dense tensor argument, after its checks."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if t.get_device() != device:
-        raise ValueError(f"{name} is on cuda:{t.get_device()}, expected cuda:{device}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    return t.data_ptr()
+    try:
+        if (t.get_device() == device and t.dtype in dtypes and t.is_contiguous() and
+                (shape is None or t.shape == shape)):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _device_of(t, name)
+    _complain(t, name, dtypes, device, shape)
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _rows(t, name, dtypes, device=None, shape=None):
-    """(address, row stride) of a 2-D argument whose rows are dense and may lie apart."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
+def _complain(t, name, dtypes, device, shape):
+    """Raises what is wrong with a CUDA tensor apart from its strides."""
     if t.dtype not in dtypes:
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {tuple(dtypes)}")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have two dimensions, not {t.dim()}")
     if device is not None and t.get_device() != device:
         raise ValueError(f"{name} is on cuda:{t.get_device()}, expected cuda:{device}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _rows(t, name, dtypes, device, shape=None):
+    """(address, row stride) of a 2-D argument whose rows are dense and may lie apart."""
+    try:
+        if (t.get_device() == device and t.dtype in dtypes and t.is_contiguous() and t.dim() == 2 and
+                (shape is None or t.shape == shape)):
+            return t.data_ptr(), t.shape[1]
+    except AttributeError:
+        pass
+    _device_of(t, name)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, not {t.dim()}")
+    _complain(t, name, dtypes, device, shape)
     rows, K = t.shape
-    if t.is_contiguous():
-        return t.data_ptr(), K
     step, unit = t.stride()
     if (unit != 1 and K > 1) or (step < K and rows > 1):
         raise ValueError(f"{name} must have dense rows (strides {t.stride()})")
     return t.data_ptr(), step if rows > 1 else K
 
 
-def _elsewhere(device, stream):
-    """Whether a call on `device` has to leave the current device or stream."""
-    return stream is not None or device != torch._C._cuda_getDevice()
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream    # of a device, as an address
 
 
 def _over_there(call, device, stream, inputs):
@@ -432,10 +437,10 @@ def quant_i8(x, sign=None, chan_scale=None, block=0, values=False, stream=None):
     x [rows][K] f32/f16/bf16; its rows may lie apart. Returns (q int8 [rows][i8_row_bytes(K)],
     scale fp32 [rows]); with values=True also scale * q in x's type, [rows][K]."""
     device = _device_of(x, "x")
-    if _elsewhere(device, stream):
+    if stream is not None or device != _current_device():
         return _over_there(lambda: quant_i8(x, sign, chan_scale, block, values), device, stream,
                            (x, sign, chan_scale))
-    px, ldx = _rows(x, "x", _DTYPES)
+    px, ldx = _rows(x, "x", _DTYPES, device)
     rows, K = x.shape
     q = x.new_empty((rows, (K + 15) // 16 * 16), dtype=torch.int8)
     scale = x.new_empty(rows, dtype=torch.float32)
@@ -445,10 +450,6 @@ def quant_i8(x, sign=None, chan_scale=None, block=0, values=False, stream=None):
                              scale.data_ptr(), v.data_ptr() if values else None,
                              _raw_stream(device)), "lq_quant_i8")
     return (q, scale, v) if values else (q, scale)
-
-
-def _raw_stream(device):
-    return torch._C._cuda_getCurrentRawStream(device)
 
 
 class Norm:
@@ -497,7 +498,7 @@ def _boundary(h, residual, post, pre, gate, gate_tokens, branch_scale, residual_
               residual_out, dtype, codes, whiten):
     """The arguments' checks, outputs and call of lq_norm_residual on the current stream."""
     device = h.get_device()
-    ph, ldh = _rows(h, "h", _DTYPES)
+    ph, ldh = _rows(h, "h", _DTYPES, device)
     rows, K = shape = h.shape
     pr, ldr, rdt = None, 0, 0
     r_out = p_out = None
@@ -562,7 +563,7 @@ def norm_residual(h, residual=None, post=None, pre=None, gate=None, gate_tokens=
     residual_out=residual updates it in place; without a residual c is only written if
     residual_out is given (else None is returned for it)."""
     device = _device_of(h, "h")
-    if _elsewhere(device, stream):
+    if stream is not None or device != _current_device():
         return _over_there(
             lambda: norm_residual(h, residual, post, pre, gate, gate_tokens, branch_scale,
                                   residual_scale, residual_out, dtype),
@@ -579,7 +580,7 @@ def norm_residual_i8(h, residual=None, post=None, pre=None, gate=None, gate_toke
     """norm_residual with n leaving as int8 rows of T(n) and their scales, as quant_i8 makes them,
     for gemm_i8. Returns (c, q, scale); with a dtype also n in that type."""
     device = _device_of(h, "h")
-    if _elsewhere(device, stream):
+    if stream is not None or device != _current_device():
         return _over_there(
             lambda: norm_residual_i8(h, residual, post, pre, gate, gate_tokens, branch_scale,
                                      residual_scale, residual_out, sign, chan_scale, block,
@@ -610,7 +611,7 @@ def gemm_i8(xq, xs, wq, ws, K=None, bias=None, dtype=torch.float32, y=None, work
     fp32. K None: the whole stored rows (quant_i8 pads them with zeros). route=None lets the
     library pick the kernel; an I8_ROUTE_* code runs that one."""
     device = _device_of(xq, "xq")
-    if _elsewhere(device, stream):
+    if stream is not None or device != _current_device():
         return _over_there(lambda: gemm_i8(xq, xs, wq, ws, K, bias, dtype, y, workspace, None,
                                            route),
                            device, stream, (xq, xs, wq, ws, bias, y, workspace))
