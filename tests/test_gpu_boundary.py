@@ -254,3 +254,72 @@ def test_block_of_8_bit_and_fractional_layers(orc, batch):
     import numpy as np
     assert_close(out.cpu().numpy(), oracle_rows(orc, layer, np.arange(200)),
                  f"block of both kinds, batch {batch}")
+
+
+@pytest.mark.parametrize("batch,K", [(1, 2048), (5, 8192), (3, 12288), (40, 1024), (300, 2048)])
+def test_back_to_back_equals_one_at_a_time(batch, K):
+    """A chain whose calls read what the ones before wrote, in place and into reused memory: run
+    without a pause, replayed as a graph, and with a wait after every call, all bits agree."""
+    g = gen(batch + K)
+    h0, r0 = rand((batch, K), F32, g, 2.0), rand((batch, K), BF16, g, 3.0)
+    pre = lq.Norm("rms", rand((K,), BF16, g, 0.2, 1.0), None, 1e-5)
+    wq, sw = lq.quant_i8(rand((K, K), BF16, g, K ** -0.5))
+    ws = lq.new_i8_workspace()
+
+    def chain(h, r, pause):
+        for _ in range(6):
+            r, q, s = lq.norm_residual_i8(h, r, pre, pre, residual_out=r, branch_scale=0.5,
+                                          block=256)
+            pause()
+            h = lq.gemm_i8(q, s, wq, sw, workspace=ws)
+            pause()
+            r, n = lq.norm_residual(h, r, None, pre, residual_out=r, dtype=F32)
+            pause()
+            q, s = lq.quant_i8(n, block=256)
+            pause()
+            h = lq.gemm_i8(q, s, wq, sw, workspace=ws)
+            pause()
+        return h, r
+
+    want = chain(h0, r0.clone(), torch.cuda.synchronize)
+    for _ in range(3):
+        got = chain(h0, r0.clone(), lambda: None)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    r1 = r0.clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = chain(h0, r1, lambda: None)
+    for _ in range(3):
+        r1.copy_(r0)
+        graph.replay()
+        assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+    assert lq.device_status(ws) == (lq.LQ_OK, 0)
+
+
+def test_two_streams_at_once():
+    """Independent chains on two streams, one workspace for both: nothing but the status is shared."""
+    g = gen(4)
+    K, N = 4096, 4096
+    w = [lq.quant_i8(rand((N, K), BF16, g, K ** -0.5)) for _ in range(2)]
+    xs = [rand((b, K), BF16, g) for b in (6, 200)]
+    ws = lq.new_i8_workspace()
+
+    def run(i):
+        x = xs[i]
+        for _ in range(8):
+            q, s = lq.quant_i8(x, block=256)
+            x = lq.gemm_i8(q, s, *w[i], dtype=BF16, workspace=ws)
+        return x
+
+    want = [run(0), run(1)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        got = []
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got.append(run(i))
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert lq.device_status(ws) == (lq.LQ_OK, 0)
