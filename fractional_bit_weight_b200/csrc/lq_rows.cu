@@ -738,7 +738,7 @@ __global__ void __launch_bounds__(Form<NV, has_r<RT>()>::kThreads, Form<NV, has_
     load_raw<HT, NV, M>(hr, a.h, row * a.ldh + off, n);
     // in flight during the first norm's reductions
     if constexpr (kHasR) load_raw<RT, NV, M>(rr, a.r, row * a.ldr + off, n);
-    if (NV > 1 && row + a.ahead < a.rows) {
+    if (NV > 1 && a.ahead < a.rows - row) {
       prefetch_row<HT>(a.h, (row + a.ahead) * a.ldh + off, n);
       if constexpr (kHasR) prefetch_row<RT>(a.r, (row + a.ahead) * a.ldr + off, n);
     }
@@ -866,9 +866,12 @@ cudaError_t launch_rows(RowArgs a, int rows, cudaStream_t st) {
   // the wide form while about all its threads are resident at once, and for rows too short to give
   // a thread of the small form four vectors
   Shape s = shape_of(a.K, block, 1);
-  // Half as many rows ahead as are in flight (2048 x 28672 codes 85 -> 76 us, 2048 x 8192 boundary
-  // 34.2 -> 31.9); a whole wave ahead or two were slower (32.5, 35.5).
-  a.ahead = std::max(1, 148 * (a.r ? 3 : 4) * 256 / 2 / std::max(1, (a.K + 31) / 32));
+  // Half as many rows ahead as are in flight (2048 x 28672 codes 86 -> 78 us, 2048 x 8192 boundary
+  // 36.9 -> 34.7; a whole wave or two ahead were slower). Not for fp32 codes without whitening,
+  // which HBM bounds as it is (8192 x 8192: 100 us, with prefetches 107).
+  a.ahead = a.plain && block == 0 && a.hdt == LQ_F32
+                ? rows
+                : std::max(1, 148 * (a.r ? 3 : 4) * 256 / 2 / std::max(1, (a.K + 31) / 32));
   a.few = (int64_t)rows * s.ctas * s.threads <= 148 * 1280;
   if (!a.few && a.K >= 1024) s = shape_of(a.K, block, 4);
   if (!vectors_ok(a)) {
