@@ -18,7 +18,8 @@
  *
  * Conventions for every entry point:
  *   - All array arguments are DEVICE pointers owned by the caller, row-major and
- *     dense. The library never allocates, frees, prints or exits.
+ *     dense (where a row stride is an argument: dense rows). The library never
+ *     allocates, frees, prints or exits.
  *   - `stream` is a cudaStream_t (NULL = the legacy default stream). Calls are
  *     asynchronous with respect to the host; results are ready when the stream is.
  *   - Arguments are checked on the host before anything is launched; a rejected
