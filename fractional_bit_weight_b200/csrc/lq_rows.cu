@@ -269,10 +269,10 @@ __device__ __forceinline__ void store_all(const float (&v)[NV][8], void* p, int 
   });
 }
 
-// the larger magnitude, NaN if either is
-__device__ __forceinline__ float max_abs(float a, float b) {
+// the largest magnitude, NaN if there is one
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
   float m;
-  asm("{\n .reg .f32 t;\n abs.f32 t, %2;\n max.NaN.f32 %0, %1, t;\n}" : "=f"(m) : "f"(a), "f"(b));
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
   return m;
 }
 
@@ -555,17 +555,24 @@ constexpr float kRound = 12582912.f;   // 1.5 * 2^23: adding it rounds half to e
 
 // Codes of eight entries as b[e] = bits of kRound + code (the low byte is the code). fma(v, 127 / a,
 // kRound) rounds a quotient that is off by at most 127 * 2^-24, so the code is right unless the
-// quotient lies within 1e-4 of a border; there border_code decides.
-__device__ __forceinline__ void codes8(const float (&v)[8], float inv, float a, uint32_t (&b)[8]) {
+// quotient lies within 2e-5 of a border; there border_code decides. Whitened entries (`exact` false)
+// carry the roundings of T, larger than that, and are left at the first answer.
+__device__ __forceinline__ void codes8(const float (&v)[8], float inv, float a, bool exact,
+                                       uint32_t (&b)[8]) {
   const float2 f = both(inv), one = both(kRound), minus = both(-1.f);
-  float worst = 0.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 m = fma2(pair(v, i), f, one);
-    const float2 d = fma2(pair(v, i), f, fma2(m, minus, one));
     b[2 * i] = __float_as_uint(m.x);
     b[2 * i + 1] = __float_as_uint(m.y);
-    worst = fmaxf(worst, fmaxf(fabsf(d.x), fabsf(d.y)));
+  }
+  if (!exact) return;
+  float worst = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 m = make_float2(__uint_as_float(b[2 * i]), __uint_as_float(b[2 * i + 1]));
+    const float2 d = fma2(pair(v, i), f, fma2(m, minus, one));
+    worst = max_abs(worst, d.x, d.y);
   }
   if (worst > 0.49998f) {
 #pragma unroll
@@ -615,7 +622,7 @@ __device__ __forceinline__ void write_codes(const RowArgs& a, const Reducer& red
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) big = max_abs(big, v[j][e]);
+    for (int i = 0; i < 4; ++i) big = max_abs(big, v[j][2 * i], v[j][2 * i + 1]);
   // across threads as bits: they order like the magnitudes, with infinity and the NaNs on top
   const uint32_t top = red.max(4, __float_as_uint(big));
   const bool finite = top < 0x7f800000u;
@@ -633,6 +640,7 @@ __device__ __forceinline__ void write_codes(const RowArgs& a, const Reducer& red
   const float inv = finite && amax > 0.f ? 127.f / as : 0.f;
   int8_t* qrow = a.q + row * a.ldq + off;
   const int qn = (int)(a.ldq - off);     // columns of the stored row from here on
+  const bool exact = a.T.block == 0;
   auto write = [&](auto t) {
     typedef decltype(t) VT;              // the type of `values`, None without
 #pragma unroll
@@ -646,7 +654,7 @@ __device__ __forceinline__ void write_codes(const RowArgs& a, const Reducer& red
         if (shift != 1.f)
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[j][e] *= shift;
-        codes8(v[j], inv, as, b);
+        codes8(v[j], inv, as, exact, b);
       }
       if constexpr (M == kStrided) {
 #pragma unroll
@@ -723,8 +731,10 @@ __global__ void __launch_bounds__(Form<NV, has_r<RT>()>::kThreads, Form<NV, has_
   __shared__ __align__(16) uint32_t slots[kReductions * 256];
   constexpr bool kHasR = has_r<RT>();
   const int T = blockDim.x;
-  const int row = (int)(blockIdx.x / (unsigned)ctas);
-  const Reducer red{slots, ctas, (int)(blockIdx.x - row * (unsigned)ctas)};
+  int row, rank;   // a row is a cluster's (of one CTA, too)
+  asm("mov.u32 %0, %clusterid.x;" : "=r"(row));
+  asm("mov.u32 %0, %cluster_ctarank;" : "=r"(rank));
+  const Reducer red{slots, ctas, rank};
   // this CTA's part of the row: n columns from column off
   const int off = red.rank * (8 * NV) * T;
   const int n = min(a.K - off, (8 * NV) * T);

@@ -289,7 +289,8 @@ LQ_API int64_t lq_i8_row_bytes(int32_t K);
 /* Symmetric int8 rows with a scale per row (the tokens of an activation, or the output channels
  * of a weight matrix). With v = T(x[t]):
  *     a = max_k |v[k]|,  scale[t] = a / 127,  q[t][k] = round(127 v[k] / a)
- * The quotient is rounded once, half to even; q lies in -127..127. A row of zeros gives scale 0
+ * The quotient is rounded once, half to even (with T, from v as fp32 holds it, to within 127 units
+ * of 2^-24); q lies in -127..127. A row of zeros gives scale 0
  * and codes 0. A row that holds an infinity or a NaN gives scale NaN and codes 0, so that it
  * reads NaN behind lq_gemm_i8.
  *   x       [rows][K] device, row t at element t * ldx (ldx >= K).
