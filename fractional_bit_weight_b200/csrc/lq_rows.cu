@@ -804,6 +804,13 @@ Shape shape_of(int K, int block, int nv) {
   const int vecs = (K + 7) / 8, most = nv == 1 ? 1024 : 256 * nv;
   s.nv = nv;
   s.ctas = (vecs + most - 1) / most;
+  // a few CTAs more where they divide the row evenly (kFull; 20480 entries: four CTAs 48.9 us,
+  // three with a ragged end 54.7)
+  for (int c = s.ctas; nv > 1 && s.ctas > 1 && c <= std::min(8, s.ctas + 2); ++c)
+    if (vecs % (32 * nv * c) == 0) {
+      s.ctas = c;
+      break;
+    }
   const int part = (vecs + s.ctas - 1) / s.ctas;
   s.threads = (std::max(1, (part + nv - 1) / nv) + 31) / 32 * 32;
   s.smem = 0;
