@@ -195,15 +195,24 @@ __device__ __forceinline__ int col_of(int j, int e) {
   return M == kStrided ? base + 32 * e + lane : base + 8 * lane + e;
 }
 
+// whether all entries of vector j of this warp's threads lie in a part of n columns
+template <int NV>
+__device__ __forceinline__ bool whole_run(int j, int n) {
+  return 8 * (int)(threadIdx.x & ~31u) * NV + 256 * (j + 1) <= n;
+}
+
 // v = entries of vector j of the row part at element `off` of p, zero from column n on
 template <class DT, int NV, Mode M>
 __device__ __forceinline__ void load_scalar(const void* p, int64_t off, int j, int n,
                                             float (&v)[8]) {
-  const typename DT::type* q = static_cast<const typename DT::type*>(p) + off;
+  const typename DT::type* q = static_cast<const typename DT::type*>(p) + off + col_of<NV, M>(j, 0);
+  constexpr int step = M == kStrided ? 32 : 1;
+  if (whole_run<NV>(j, n)) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int c = col_of<NV, M>(j, e);
-    v[e] = c < n ? to_f32(q[c]) : 0.f;
+    for (int e = 0; e < 8; ++e) v[e] = to_f32(q[e * step]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = col_of<NV, M>(j, e) < n ? to_f32(q[e * step]) : 0.f;
   }
 }
 
@@ -237,9 +246,16 @@ __device__ __forceinline__ void store8(void* p, int64_t off, int j, int n, const
                         pack2<DT>(v[6], v[7]));
     }
   } else {
+    q += col_of<NV, M>(j, 0);
+    constexpr int step = M == kStrided ? 32 : 1;
+    if (whole_run<NV>(j, n)) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (col_of<NV, M>(j, e) < n) from_f32(v[e], q[col_of<NV, M>(j, e)]);
+      for (int e = 0; e < 8; ++e) from_f32(v[e], q[e * step]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (col_of<NV, M>(j, e) < n) from_f32(v[e], q[e * step]);
+    }
   }
 }
 
@@ -657,9 +673,14 @@ __device__ __forceinline__ void write_codes(const RowArgs& a, const Reducer& red
         codes8(v[j], inv, as, exact, b);
       }
       if constexpr (M == kStrided) {
+        if (whole_run<NV>(j, qn)) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (col_of<NV, M>(j, e) < qn) qrow[col_of<NV, M>(j, e)] = (int8_t)b[e];
+          for (int e = 0; e < 8; ++e) qrow[c + 32 * e] = (int8_t)b[e];
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (c + 32 * e < qn) qrow[c + 32 * e] = (int8_t)b[e];
+        }
       } else {
         *reinterpret_cast<uint2*>(qrow + c) =
             make_uint2(low_bytes(b[0], b[1], b[2], b[3]), low_bytes(b[4], b[5], b[6], b[7]));
