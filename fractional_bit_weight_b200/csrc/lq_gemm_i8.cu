@@ -57,9 +57,17 @@ __device__ __forceinline__ void store_y(const Args& a, int64_t i, float v) {
 
 // ------------------------------------------------------------------ few tokens
 
+// Loads that stay behind grid_wait: a read-only (.nc) load may be moved ahead of it.
 __device__ __forceinline__ uint4 ld_weights(const int8_t* p) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.L2::128B.v4.u32 {%0,%1,%2,%3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.L2::128B.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
+__device__ __forceinline__ uint4 ld_token(const int8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
   return v;
 }
@@ -76,7 +84,7 @@ __device__ __forceinline__ void mma_16832(int (&c)[4], uint32_t a0, uint32_t a1,
 __device__ __forceinline__ uint4 ld_token_end(const int8_t* row, int k, int K) {
   uint4 v = make_uint4(0u, 0u, 0u, 0u);
   if (k >= K) return v;
-  v = __ldg(reinterpret_cast<const uint4*>(row + k));
+  v = ld_token(row + k);
   uint32_t* w = reinterpret_cast<uint32_t*>(&v);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -122,7 +130,7 @@ __global__ void __launch_bounds__(512) gemv_w8_kernel(const __grid_constant__ Ar
     for (int s = 0; s < U; ++s)
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(x[i] + k + 64 * s));
+        const uint4 v = ld_token(x[i] + k + 64 * s);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
           mma_16832(c[m][i], u[s][m][0].x, u[s][m][1].x, u[s][m][0].y, u[s][m][1].y, v.x, v.y);

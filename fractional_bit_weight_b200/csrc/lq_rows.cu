@@ -128,6 +128,20 @@ __device__ __forceinline__ uint4 ld_stream(const void* p) {
   return v;
 }
 
+// 16 and 8 bytes that every row reads; not read-only (.nc) loads, which may be moved ahead of a wait
+// for the kernel before
+__device__ __forceinline__ uint4 ld_kept(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint2 ld_kept(const uint2* p) {
+  uint2 v;
+  asm volatile("ld.global.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+
 template <class DT>
 __device__ __forceinline__ void unpack2(uint32_t w, float& lo, float& hi) {
   if constexpr (DT::dt == LQ_BF16) {
@@ -223,8 +237,8 @@ __device__ __forceinline__ void load_shared8(const void* p, int64_t off, int j, 
   if constexpr (is_vec(M)) {
     const uint4* s = reinterpret_cast<const uint4*>(static_cast<const typename DT::type*>(p) + off +
                                                     col_of<NV, M>(j, 0));
-    const uint4 a = __ldg(s);
-    unpack8<DT>(a, DT::size == 4 ? __ldg(s + 1) : a, v);
+    const uint4 a = ld_kept(s);
+    unpack8<DT>(a, DT::size == 4 ? ld_kept(s + 1) : a, v);
   } else {
     load_scalar<DT, NV, M>(p, off, j, n, v);
   }
@@ -461,7 +475,7 @@ __device__ __forceinline__ void apply_whiten(float (&v)[NV][8], const Whiten& T,
       if (T.sign) {
         uint32_t lo, hi;
         if (is_vec(M)) {
-          const uint2 s = __ldg(reinterpret_cast<const uint2*>(T.sign + off + c));
+          const uint2 s = ld_kept(reinterpret_cast<const uint2*>(T.sign + off + c));
           lo = s.x;
           hi = s.y;
         } else {
@@ -525,7 +539,7 @@ __device__ __forceinline__ void whiten_mma(float (&v)[NV][8], const uint4 (&raw)
     const int c = col_of<NV, M>(j, 0);
     uint32_t w[4] = {raw[j][0].x, raw[j][0].y, raw[j][0].z, raw[j][0].w};
     if (T.sign && in_row<M>(c, n)) {
-      const uint2 s = __ldg(reinterpret_cast<const uint2*>(T.sign + off + c));
+      const uint2 s = ld_kept(reinterpret_cast<const uint2*>(T.sign + off + c));
       // the sign bits of bytes 0, 1 and of 2, 3 over those of a pair of entries
       w[0] ^= __byte_perm(s.x, 0u, 0x1404) & 0x80008000u;
       w[1] ^= __byte_perm(s.x, 0u, 0x3424) & 0x80008000u;

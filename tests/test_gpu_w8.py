@@ -341,6 +341,38 @@ def test_other_streams():
         assert torch.equal(y, y2)
 
 
+def test_call_while_another_device_is_current(monkeypatch):
+    """With another device current, a call makes its tensors' device current and runs there."""
+    entered = []
+    real = torch.cuda.device
+
+    class Spy(real):
+        def __enter__(self):
+            entered.append(self.idx)
+            return super().__enter__()
+
+    x = rand(3, 256, BF16, 1)
+    wq, sw = int8(8, 256, 1), scales(8, 1)
+    q, s = lq.quant_i8(x)
+    y = lq.gemm_i8(q, s, wq, sw)
+    r, n = lq.norm_residual(x, x, None, lq.Norm("rms"))
+    monkeypatch.setattr(torch.cuda, "device", Spy)
+
+    def elsewhere():
+        answers = iter((torch.cuda.current_device() + 1, torch.cuda.current_device()))
+        monkeypatch.setattr(lq, "_current_device", lambda: next(answers))
+
+    elsewhere()
+    q2, s2 = lq.quant_i8(x)
+    elsewhere()
+    y2 = lq.gemm_i8(q, s, wq, sw)
+    elsewhere()
+    r2, n2 = lq.norm_residual(x, x, None, lq.Norm("rms"))
+    assert entered == [x.get_device()] * 3
+    assert torch.equal(q, q2) and torch.equal(s, s2) and torch.equal(y, y2)
+    assert torch.equal(r, r2) and torch.equal(n, n2)
+
+
 def test_refused_tensors():
     x = rand(4, 64, BF16, 1)
     q, s = lq.quant_i8(x)
