@@ -154,6 +154,37 @@ def test_in_place_and_strides(K):
     assert torch.equal(n, h * 0.5) and torch.equal(c, (h * 0.5).to(BF16))
 
 
+@pytest.mark.parametrize("rows,K", [(3, 100), (3, 4096), (600, 1000), (600, 2048), (2, 20000),
+                                    (300, 9001)])
+def test_outputs_stay_inside(rows, K):
+    """Nothing is written before or behind any output."""
+    g = gen(K)
+    h, r = rand((rows, K), F32, g), rand((rows, K), BF16, g)
+    ks = lq.i8_row_bytes(K)
+
+    def guarded(shape, dtype, fill):
+        n = 1
+        for d in shape:
+            n *= d
+        flat = torch.full((n + 256,), fill, dtype=dtype, device=DEV)
+        return flat, flat[128:128 + n].view(shape)
+
+    bufs = [guarded((rows, K), BF16, 3.0), guarded((rows, K), F16, 4.0),
+            guarded((rows, ks), torch.int8, 55), guarded((rows,), F32, 6.0)]
+    c, n, q, s = (v for _, v in bufs)
+    pre = lq.Norm("layer", None, None, 1e-5)
+    rc = lq.lib().lq_norm_residual(
+        h.data_ptr(), lq.LQ_F32, K, r.data_ptr(), lq.LQ_BF16, K, rows, K, pre._ref, None, 1.0, 1.0,
+        c.data_ptr(), pre._ref, n.data_ptr(), lq.LQ_F16, None, q.data_ptr(), s.data_ptr(),
+        torch.cuda.current_stream().cuda_stream)
+    assert rc == lq.LQ_OK
+    for (flat, _), fill in zip(bufs, (3.0, 4.0, 55, 6.0)):
+        assert (flat[:128] == fill).all() and (flat[-128:] == fill).all()
+    c2, q2, s2, n2 = lq.norm_residual_i8(h, r, pre, pre, dtype=F16)
+    for got, want in ((c, c2), (n, n2), (q, q2), (s, s2)):
+        assert torch.equal(got, want)
+
+
 def test_weights_off_alignment():
     K = 512
     g = gen(1)

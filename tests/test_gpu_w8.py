@@ -111,6 +111,33 @@ def test_quant_strides_and_alignment():
         check_exact(x, q, scale, values)
 
 
+def check_whitened(x, sign, chan, block):
+    K = x.shape[1]
+    q, scale, values = lq.quant_i8(x, sign=sign, chan_scale=chan, block=block, values=True)
+    v, dv = ref.whiten(x, sign, chan, block)
+    a = v.abs().amax(1)
+    da = dv.amax(1)
+    assert ((scale.double() - a / 127).abs() <= (da + 2 * ref.EPS32 * a) / 127).all()
+    # the code is the rounding of a quotient whose entry and maximum are off by dv and da
+    off = 127 * (dv + da[:, None]) / (a - da)[:, None] + 1e-12
+    assert ((q[:, :K].double() - 127 * v / a[:, None]).abs() <= 0.5 + off).all()
+    assert not q[:, K:].any()
+    assert torch.equal(values, (q[:, :K].float() * scale[:, None]).to(x.dtype))
+
+
+@pytest.mark.parametrize("rows", [2, 500])
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("block", [4, 64, 256, 1024])
+def test_quant_whitened_off_alignment(rows, dtype, block):
+    """Rows that start off a 16-byte boundary, and signs and scales that do."""
+    base = rand(rows, 2400, dtype, rows + block)
+    sg, cs = signs(2050, 1), torch.rand(2050, device=DEV) + 0.5
+    for x in (base[:, 1:1025], base[:, 3:2051], base[:, 8:1032]):
+        K = x.shape[1]
+        check_whitened(x, sg[1:K + 1], None, block)
+        check_whitened(x, sg[1:K + 1].clone(), cs[1:K + 1], block)
+
+
 @pytest.mark.parametrize("block,K", [(1, 24), (2, 30), (4, 100), (8, 8), (16, 48), (32, 32),
                                      (64, 320), (128, 1152), (256, 256), (256, 8192),
                                      (256, 28672), (512, 1536), (1024, 5120), (2048, 2048),
@@ -121,16 +148,7 @@ def test_quant_whitened(block, K, rows, dtype):
     x[0, 1] = 30.0
     cs = torch.rand(K, device=DEV) + 0.5
     for sign, chan in ((signs(K, 2), None), (signs(K, 3), cs), (None, None)):
-        q, scale, values = lq.quant_i8(x, sign=sign, chan_scale=chan, block=block, values=True)
-        v, dv = ref.whiten(x, sign, chan, block)
-        a = v.abs().amax(1)
-        da = dv.amax(1)
-        assert ((scale.double() - a / 127).abs() <= (da + 2 * ref.EPS32 * a) / 127).all()
-        # the code is the rounding of a quotient whose entry and maximum are off by dv and da
-        off = 127 * (dv + da[:, None]) / (a - da)[:, None] + 1e-12
-        assert ((q[:, :K].double() - 127 * v / a[:, None]).abs() <= 0.5 + off).all()
-        assert not q[:, K:].any()
-        assert torch.equal(values, (q[:, :K].float() * scale[:, None]).to(dtype))
+        check_whitened(x, sign, chan, block)
 
 
 def test_quant_outputs_stay_inside():
