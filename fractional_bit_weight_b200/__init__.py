@@ -342,7 +342,7 @@ def codebook_round(w, M, d, D, mode=0, b=None, mse=None, workspace=None, stream=
 # ---- 8-bit linear layers and the block boundaries around them (include/liblq.h)
 
 GEMM_I8_WORKSPACE_BYTES = 256   # LQ_GEMM_I8_WORKSPACE_BYTES
-I8_ROUTE_GEMV, I8_ROUTE_TC, I8_ROUTE_PAIR = 0, 1, 2
+I8_ROUTE_GEMV, I8_ROUTE_TC, I8_ROUTE_PAIR, I8_ROUTE_SPLIT = 0, 1, 2, 3
 _F32 = (torch.float32,)
 _I8 = (torch.int8,)
 _NORM_KINDS = {"rms": 1, "layer": 2}

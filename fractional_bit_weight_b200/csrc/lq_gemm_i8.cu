@@ -19,8 +19,10 @@
 //    and a warp stores 32 consecutive outputs of a token. Copies and MMAs are issued by an elected
 //    lane each (64 tokens x 8192 x 8192: 30 -> 20 us against a lane chosen by its number).
 //    Measured (device): 2048 tokens 8192 -> 28672 292 us, 3.29 Pop/s, tensor pipe 86 % busy at the
-//    1.56 GHz that the power limit leaves (347 us in a loop of calls); 16 tokens 28672 -> 8192
-//    38.9 us, 6.07 TB/s (0.93 of the copy rate); 77 tokens 4100 -> 1003 7.9 us, most of it start.
+//    1.56 GHz that the power limit leaves (341 us in a loop of calls); 16 tokens 28672 -> 8192
+//    38.4 us, 6.14 TB/s (0.94 of the copy rate). A layer of few tiles is split along K over the
+//    CTAs of a cluster, which add their sums up through distributed shared memory: 32 tokens 8192
+//    -> 1024 5.9 us (9.6 unsplit), 20 tokens 28672 -> 1024 9.2 us (26.1).
 // Every wait on an mbarrier is bounded in time: on expiry the kernel records LQ_ETIMEOUT in the
 // workspace status word, the roles leave their loops, in-flight copies and MMAs are waited for
 // (again bounded) and tensor memory is released before the CTA exits.
@@ -220,11 +222,16 @@ constexpr int kThreads = 7 * 32;
 constexpr int kTmemCols = 2 * kMaxTokens;
 constexpr uint64_t kWaitNs = 2000000000ull;
 
+// kOne: one CTA per tile. kPair: two CTAs on one tile of twice the rows. kSplit: a cluster of CTAs
+// on one tile, each over a part of K.
+enum Kind { kOne, kPair, kSplit };   // LQ_I8_ROUTE_TC and the routes behind it
+
 // One call's tiles over all of K, in stages of `chunks` 128-byte chunks. A tile is `tokens` tokens
 // x `rows` weight rows per CTA (a pair of CTAs takes twice the rows, and each fetches half of the
 // tokens). A stage in shared memory: [chunks][rows][128 B], then [chunks][fetched tokens][128 B].
 struct Plan {
-  int pair;                  // 1: CTA pairs
+  int kind;                  // kOne, kPair, kSplit
+  int split, cols;           // kSplit: CTAs along K, tokens that each of them finishes (of 4)
   int rows, tokens;          // at most 128 and 256; multiples of 8 and of 16 (pairs: 32)
   int tiles_n, tiles_t, tiles;
   int chunks, nks, stages;   // chunks per stage, stages per tile, ring slots
@@ -355,19 +362,82 @@ __device__ __forceinline__ void write_tile(const Args& a, uint32_t taddr, int n,
   }
 }
 
+// The token scales of token tile tt into a warp's copy, zero behind the batch.
+__device__ __forceinline__ void load_scales(const Args& a, const Plan& p, int tt, float* sx) {
+  const int t0 = tt * p.tokens;
+  for (int i = threadIdx.x & 31; i < p.tokens; i += 32)
+    sx[i] = t0 + i < a.batch ? a.xs[t0 + i] : 0.f;
+  __syncwarp();
+}
+
+// kSplit: this warp's 32 rows of the CTA's partial sums, four tokens at a time to the CTA of the
+// cluster that finishes them: part there is [CTA they come from][its tokens / 4][128 rows][4].
+__device__ __forceinline__ void send_partials(uint32_t taddr, int* part, const Plan& p, int krank,
+                                              int row, int nt) {
+  int to = 0, col = 0;
+#pragma unroll 1
+  for (int c = 0; c < nt; c += 32) {
+    uint32_t r[32];
+    tmem_ld_32x32b_x32(taddr + (uint32_t)c, r);
+    tmem_ld_wait();
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+      if (c + j < nt) {
+        const uint32_t at = cluster_addr(part + (krank * p.cols + col) * kMmaM + row * 4, to);
+        asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(r[j]),
+                     "r"(r[j + 1]), "r"(r[j + 2]), "r"(r[j + 3])
+                     : "memory");
+      }
+      col += 4;
+      if (col == p.cols) {
+        col = 0;
+        ++to;
+      }
+    }
+  }
+}
+
+template <class YT>
+__device__ __forceinline__ void finish_split(const Args& a, const Plan& p, const int* part,
+                                             int krank, int row, int n, int t0, int nt,
+                                             const float* sx, float sw, float bias) {
+  const int first = krank * p.cols, end = min(p.cols, nt - first);
+  YT* y = static_cast<YT*>(a.y) + (int64_t)(t0 + first) * a.N + n;
+  for (int c = 0; c < end; c += 4) {
+    int4 sum = make_int4(0, 0, 0, 0);
+    for (int s = 0; s < p.split; ++s) {
+      const int4 v = *reinterpret_cast<const int4*>(part + (s * p.cols + c) * kMmaM + row * 4);
+      sum.x += v.x;
+      sum.y += v.y;
+      sum.z += v.z;
+      sum.w += v.w;
+    }
+    const int total[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (c + j < end)
+        put_y(y + (int64_t)(c + j) * a.N, fmaf((float)total[j], sx[first + c + j] * sw, bias));
+  }
+}
+
 // An MMA always takes 128 rows of A from a CTA's shared memory. A tile of fewer rows leaves the
 // rest to whatever lies behind it there (the ring ends 16 KB before the allocation does): those
 // lanes of the accumulator are never read.
 //
-// PAIR: two CTAs work on one tile of twice the rows (cta_group::2). The even CTA's barriers count
+// kPair: two CTAs work on one tile of twice the rows (cta_group::2). The even CTA's barriers count
 // the copies of both, its MMA thread issues for both, and commits arrive in both. Each SM then
 // reads and fills 16 KB less shared memory per 128 inputs of a 256-token tile: one CTA alone moves
 // 24 KB per MMA through it, 192 clocks against the MMA's 128.
-template <bool PAIR>
+//
+// kSplit: each CTA of a cluster sums its part of K of the same tile, then they hand the int32
+// partials out over distributed shared memory, every CTA finishing a range of the tokens. For
+// layers too small to fill the SMs with tiles, whose time would be one SM's way through all of K.
+template <int KIND>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_w8_kernel(const __grid_constant__ CUtensorMap tmap_w,
                    const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ Args a,
                    const __grid_constant__ Plan p) {
+  constexpr bool PAIR = KIND == kPair, SPLIT = KIND == kSplit;
   extern __shared__ uint8_t smem_raw[];
   Ctl* ctl = reinterpret_cast<Ctl*>(smem_raw);
   uint8_t* ring = reinterpret_cast<uint8_t*>(
@@ -376,7 +446,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kCtas = PAIR ? 2 : 1;
   const int rank = PAIR ? (int)(blockIdx.x & 1) : 0;    // clusters are consecutive pairs
-  const int first = (int)blockIdx.x / kCtas, step = (int)gridDim.x / kCtas;
+  const int group = PAIR ? 2 : SPLIT ? p.split : 1;     // CTAs of a tile
+  const int krank = SPLIT ? (int)blockIdx.x % group : 0;
+  const int first = (int)blockIdx.x / group, step = (int)gridDim.x / group;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
@@ -406,7 +478,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < kEpiWarps) {
     // ---------------------------------------------------------------- epilogue
     int lt = 0;
-    for (int tile = first; tile < p.tiles; tile += step, ++lt) {
+    if constexpr (SPLIT) {
+      load_scales(a, p, first % p.tiles_t, ctl->scale[warp]);
+      if (!__all_sync(0xffffffffu, wait_phase(&ctl->tmem_full[0], 0, abort, true)))
+        give_up(ctl, a.status);
+    }
+    for (int tile = first; !SPLIT && tile < p.tiles; tile += step, ++lt) {
       const int tn = tile / p.tiles_t, tt = tile - tn * p.tiles_t;
       const int b = lt & 1;
       const int row = warp * 32 + lane, n = (tn * kCtas + rank) * p.rows + row;
@@ -417,8 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float bias = ok && a.bias ? a.bias[n] : 0.f;
       float* sx = ctl->scale[warp];
       __syncwarp();
-      for (int i = lane; i < p.tokens; i += 32) sx[i] = i < nt ? a.xs[t0 + i] : 0.f;
-      __syncwarp();
+      load_scales(a, p, tt, sx);
       if (!__all_sync(0xffffffffu, wait_phase(&ctl->tmem_full[b], (lt >> 1) & 1, abort, true))) {
         give_up(ctl, a.status);
         break;
@@ -459,10 +535,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           uint8_t* at = base + slot.at * p.stage_bytes;
+          const int ks = krank * p.nks + k;   // past the end of K a copy brings zeros
           if (rank == 0) mbar_arrive_expect_tx(&ctl->full[slot.at], bytes);
           const uint32_t full = PAIR ? cluster_addr(&ctl->full[slot.at], 0) : 0u;
           for (int c = 0; c < (p.wide ? 1 : p.chunks); ++c) {
-            const int x = p.wide ? 0 : (k * p.chunks + c) * BK, z = p.wide ? k * p.chunks : 0;
+            const int x = p.wide ? 0 : (ks * p.chunks + c) * BK, z = p.wide ? ks * p.chunks : 0;
             if constexpr (PAIR) tma_load_3d_pair(at + c * rows * BK, tmap, full, x, row, z);
             else tma_load_3d(at + c * rows * BK, tmap, &ctl->full[slot.at], x, row, z);
           }
@@ -528,6 +605,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   }
 
+  if constexpr (SPLIT) {
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();   // all MMAs of the cluster are done: the rings hold partials from here on
+    tc_fence_after();
+    int* part = reinterpret_cast<int*>(ring);
+    const int tn = first / p.tiles_t, t0 = (first - tn * p.tiles_t) * p.tokens;
+    const int nt = min(p.tokens, a.batch - t0), row = warp * 32 + lane, n = tn * p.rows + row;
+    const bool ok = warp < kEpiWarps && row < p.rows && n < a.N;
+    const float sw = ok ? a.ws[n] : 0.f, bias = ok && a.bias ? a.bias[n] : 0.f;
+    if (warp < kEpiWarps && warp * 32 < p.rows)
+      send_partials(tmem + ((uint32_t)(warp * 32) << 16), part, p, krank, row, nt);
+    cluster_sync();
+    if (ok) {
+      const float* sx = ctl->scale[warp];
+      if (a.ydt == LQ_BF16)
+        finish_split<__nv_bfloat16>(a, p, part, krank, row, n, t0, nt, sx, sw, bias);
+      else if (a.ydt == LQ_F16)
+        finish_split<__half>(a, p, part, krank, row, n, t0, nt, sx, sw, bias);
+      else
+        finish_split<float>(a, p, part, krank, row, n, t0, nt, sx, sw, bias);
+    }
+    __syncwarp();
+  }
   tc_fence_before();
   __syncthreads();
   if constexpr (PAIR) cluster_sync();   // neither CTA's memory is in use by the other any more
@@ -541,6 +642,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ------------------------------------------------------------------ host side
 
 constexpr size_t kMaxSmem = 227 * 1024;
+constexpr int kMaxSplit = 8;                // CTAs of a cluster along K
+constexpr int kSplitTokens = 128;           // tokens of a kSplit tile: its partials fit the ring
+constexpr int kSplitFit[] = {0, 148, 74, 0, 33, 0, 0, 0, 15};   // clusters of 2, 4 and 8 CTAs that
+                                            // are resident at once on 148 SMs, see make_plan
 constexpr int32_t kMost = 1 << 30;          // tokens, rows: tile coordinates stay in 32 bits
 
 // The tile of a call. Rows of a tile are chosen so that its tiles fill whole waves of the SMs: few
@@ -552,13 +657,42 @@ constexpr int32_t kMost = 1 << 30;          // tokens, rows: tile coordinates st
 // (1.67 clocks each), whichever is longest; per wave 6000; for the last epilogue 33 per token; for
 // a pair's start 4800. Pairs: 2048 x 8192 x 28672 308 against 344 us, 128 x 4096 x 4096 10.2
 // against 9.7 us.
-Plan make_plan(int batch, int K, int N, int sms, int force_pair = -1) {
+//
+// Clusters along K are taken while they are all resident at once: the sixteenth cluster of 8 waits
+// for the first (15 of them 8.2 us, 16 14.6), as the 34th of 4 does (33 10.9, 34 19.1). Their
+// estimate is fitted to 51 layers of 128 to 8192 rows with 16 to 2000 tokens (the tile picked was
+// within 1.2 % of the fastest on average, 9 % at worst). Split against whole: 32 x 8192 x 1024 6.3
+// against 9.9 us, 20 x 28672 x 1024 10.0 against 26.4, 64 x 14336 x 4096 15.2 against 18.9, 512 x
+// 4096 x 1024 9.2 against 11.3; and 24 x 1024 x 1024 4.3 against 3.5, 64 x 8192 x 8192 16.5
+// against 15.8.
+Plan make_plan(int batch, int K, int N, int sms, int force = -1) {
   Plan best{};
   double best_cost = 0;
   const int chunks_k = (K + BK - 1) / BK;
-  for (int pair = 0; pair < 2; ++pair) {
-    if (force_pair >= 0 && pair != force_pair) continue;
-    const int ctas = pair ? 2 : 1, units = sms / ctas, unit = 16 * ctas;
+  auto consider = [&](int kind, int split, int rows, int tokens, int64_t tn, int tt, int64_t waves) {
+    const int shared = kind == kPair ? 2 : 1;          // CTAs that share a tile's tokens
+    const int fetched = rows + tokens / shared;
+    const double mma = std::max(160.0, 2.0 * tokens);
+    const double smem = 0.82 * (kMmaM + tokens / shared + fetched);
+    const double step = std::max({mma, smem, 1.67 * fetched});
+    double cost;
+    if (kind == kSplit)
+      cost = (double)waves * (1.36 * ((chunks_k + split - 1) / split) * step + 53.0 * tokens +
+                              35.0 * tokens / split + 7070);
+    else
+      cost = (double)waves * (chunks_k * step + 6000) + 33.0 * tokens + (kind == kPair ? 4800.0 : 0.0);
+    if (best.tokens != 0 && cost >= best_cost) return;
+    best_cost = cost;
+    best.kind = kind;
+    best.split = split;
+    best.rows = rows;
+    best.tokens = tokens;
+    best.tiles_n = (int)tn;
+    best.tiles_t = tt;
+  };
+  for (int kind : {kOne, kPair}) {
+    if (force >= 0 && kind != force) continue;
+    const int ctas = kind == kPair ? 2 : 1, units = sms / ctas, unit = 16 * ctas;
     int last = 0;
     for (int tiles_t = (batch + kMaxTokens - 1) / kMaxTokens, tries = 0; tries < 4; ++tiles_t, ++tries) {
       const int tokens = ((batch + tiles_t - 1) / tiles_t + unit - 1) / unit * unit;
@@ -574,31 +708,40 @@ Plan make_plan(int batch, int K, int N, int sms, int force_pair = -1) {
       if (rows * 8 >= kMmaM * 7) rows = kMmaM;
       tn = (N + ctas * rows - 1) / (ctas * rows);
       waves = (tn * tt + units - 1) / units;
-      const int fetched = rows + tokens / ctas;
-      const double mma = 2.0 * tokens, smem = 0.82 * (kMmaM + tokens / ctas + fetched);
-      const double cost = pair * 4800.0 + 33.0 * tokens +
-                          (double)waves * (chunks_k * std::max({mma, smem, 1.67 * fetched}) + 6000);
-      if (best.tokens == 0 || cost < best_cost) {
-        best_cost = cost;
-        best.pair = pair;
-        best.rows = rows;
-        best.tokens = tokens;
-        best.tiles_n = (int)tn;
-        best.tiles_t = tt;
-      }
+      consider(kind, 1, rows, tokens, tn, tt, waves);
     }
   }
-  const int fetched = best.tokens / (best.pair ? 2 : 1);
+  // clusters along K: the fewest tokens with which all of them are resident at once
+  for (int split = 2; split <= kMaxSplit && (force < 0 || force == kSplit); split *= 2) {
+    const int64_t full = (N + kMmaM - 1) / kMmaM, fit = std::max(1, kSplitFit[split] * sms / 148);
+    const int64_t most = std::max<int64_t>(1, fit / full);       // token tiles
+    const int tokens = (int)std::min<int64_t>(kSplitTokens, ((batch + most - 1) / most + 15) / 16 * 16);
+    const int tt = (batch + tokens - 1) / tokens;
+    // tiles of 128 rows, or of fewer on all SMs
+    for (int64_t tn : {full, fit / tt}) {
+      if (tn < full) continue;
+      const int rows = (int)((N + tn - 1) / tn + 7) / 8 * 8;
+      tn = (N + rows - 1) / rows;
+      const int64_t waves = (tn * tt + fit - 1) / fit;
+      if (force >= 0 || waves == 1) consider(kSplit, split, rows, tokens, tn, tt, waves);
+    }
+  }
+  const int fetched = best.tokens / (best.kind == kPair ? 2 : 1);
   best.tiles = best.tiles_n * best.tiles_t;
+  best.cols = ((best.tokens + best.split - 1) / best.split + 3) / 4 * 4;
   // stages of up to 48 KB, four of them at least
-  best.chunks = std::max(1, std::min({kMaxChunks, chunks_k, 48 * 1024 / ((best.rows + fetched) * BK)}));
+  best.chunks = std::max(1, std::min({kMaxChunks, (chunks_k + best.split - 1) / best.split,
+                                      48 * 1024 / ((best.rows + fetched) * BK)}));
   best.wide = K % BK == 0;
   best.a_bytes = best.chunks * best.rows * BK;
   best.stage_bytes = best.a_bytes + best.chunks * fetched * BK;
-  best.nks = (chunks_k + best.chunks - 1) / best.chunks;
+  best.nks = ((chunks_k + best.chunks - 1) / best.chunks + best.split - 1) / best.split;
   const size_t fixed = sizeof(Ctl) + 1024 + (size_t)kMmaM * BK;
   best.stages = (int)std::min<size_t>(kMaxStages, (kMaxSmem - fixed) / best.stage_bytes);
-  best.smem = fixed + (size_t)best.stages * best.stage_bytes;
+  size_t ring = (size_t)best.stages * best.stage_bytes;
+  if (best.kind == kSplit)   // the partials take the ring's place
+    ring = std::max(ring, (size_t)best.split * best.cols * kMmaM * sizeof(int));
+  best.smem = fixed + ring;
   return best;
 }
 
@@ -621,22 +764,26 @@ bool encode_rows(CUtensorMap* m, const int8_t* p, int64_t K, int64_t rows, int64
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-cudaError_t launch_tc(const Args& a, int force_pair, cudaStream_t st) {
+cudaError_t launch_tc(const Args& a, int force, cudaStream_t st) {
   const int sms = tc_sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
   if ((int64_t)((a.N + 127) / 128) * ((a.batch + 15) / 16) > (1 << 30)) return cudaErrorInvalidValue;
-  const Plan p = make_plan(a.batch, a.K, a.N, sms, force_pair);
-  static int smem_set[2][64];
-  const void* kernel = p.pair ? (const void*)gemm_w8_kernel<true> : (const void*)gemm_w8_kernel<false>;
-  cudaError_t e = ensure_smem(kernel, p.smem, smem_set[p.pair]);
+  const Plan p = make_plan(a.batch, a.K, a.N, sms, force);
+  static int smem_set[3][64];
+  const void* kernels[3] = {(const void*)gemm_w8_kernel<kOne>, (const void*)gemm_w8_kernel<kPair>,
+                            (const void*)gemm_w8_kernel<kSplit>};
+  cudaError_t e = ensure_smem(kernels[p.kind], p.smem, smem_set[p.kind]);
   if (e != cudaSuccess) return e;
-  const int ctas = p.pair ? 2 : 1;
+  const int shared = p.kind == kPair ? 2 : 1;              // CTAs that share a tile's tokens
+  const int group = p.kind == kPair ? 2 : p.split;         // CTAs of a cluster
+  if ((int64_t)p.tiles * group > INT32_MAX) return cudaErrorInvalidValue;
   CUtensorMap tw, tx;
   if (!encode_rows(&tw, a.wq, a.K, a.N, a.ld, p.rows, p.chunks) ||
-      !encode_rows(&tx, a.xq, a.K, a.batch, a.ld, p.tokens / ctas, p.chunks))
+      !encode_rows(&tx, a.xq, a.K, a.batch, a.ld, p.tokens / shared, p.chunks))
     return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(ctas * std::min(p.tiles, sms / ctas));
+  // persistent, except that a cluster along K takes one tile
+  cfg.gridDim = dim3(group * (p.kind == kSplit ? p.tiles : std::min(p.tiles, sms / group)));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = p.smem;
   cfg.stream = st;
@@ -644,20 +791,25 @@ cudaError_t launch_tc(const Args& a, int force_pair, cudaStream_t st) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.x = group;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1 + p.pair;
-  return p.pair ? cudaLaunchKernelEx(&cfg, gemm_w8_kernel<true>, tw, tx, a, p)
-                : cudaLaunchKernelEx(&cfg, gemm_w8_kernel<false>, tw, tx, a, p);
+  cfg.numAttrs = group > 1 ? 2 : 1;
+  return p.kind == kPair    ? cudaLaunchKernelEx(&cfg, gemm_w8_kernel<kPair>, tw, tx, a, p)
+         : p.kind == kSplit ? cudaLaunchKernelEx(&cfg, gemm_w8_kernel<kSplit>, tw, tx, a, p)
+                            : cudaLaunchKernelEx(&cfg, gemm_w8_kernel<kOne>, tw, tx, a, p);
 }
 
-// Few tokens go to the GEMV, whose start is shorter: at 8 tokens 5.2 against 10.2 us on 1024 x 8192,
-// 40.7 against 39.4 us on 28672 x 8192. Its loads of the tokens grow with the batch: at 16 tokens
-// 6.3 against 7.3 us on 4096 x 4096 and 15.5 against 15.8 on 8192 x 8192, but 47.8 against 40.1 us
-// on 28672 x 8192; at 24 tokens 19.5 against 16.0 us on 8192 x 8192.
+// Few tokens go to the GEMV, whose start is shorter: at 8 tokens 2.9 against 4.7 us on 4096 x 1024,
+// 37.9 against 38.6 us on 28672 x 8192. Its loads of the tokens grow with the batch: at 16 tokens
+// 4.9 against 6.5 us on 4096 x 4096, 11.8 against 12.2 on 12288 x 4096, but 14.1 against 13.9 on
+// 14336 x 4096, 15.0 against 14.3 on 8192 x 8192 and 43.3 against 38.7 us on 28672 x 8192. With a
+// CTA per 16 rows it leaves half the SMs idle on a layer of up to 1184 rows, where clusters along K
+// win on long ones: at one token 3.8 against 5.1 us on 8192 x 1024, 6.1 against 6.1 us on 14336 x
+// 1024, 12.5 against 8.6 us on 28672 x 1024.
 bool few_tokens(int32_t batch, int32_t K, int32_t N) {
-  return batch <= 8 || (batch <= LQ_I8_GEMV_MAX_BATCH && (int64_t)N * K <= 80 * 1000 * 1000);
+  if (batch > LQ_I8_GEMV_MAX_BATCH || (N <= 16 * 74 && K > 14336)) return false;
+  return batch <= 8 || (int64_t)N * K <= 54 * 1000 * 1000;
 }
 
 cudaError_t launch(const Args& a, int route, cudaStream_t st) {
@@ -665,7 +817,7 @@ cudaError_t launch(const Args& a, int route, cudaStream_t st) {
     if (a.batch <= 8) return launch_gemv<1, 1, 2>(a, st);
     return launch_gemv<1, 2, 4>(a, st);
   }
-  return launch_tc(a, route < 0 ? -1 : route == LQ_I8_ROUTE_PAIR, st);
+  return launch_tc(a, route < 0 ? -1 : route - LQ_I8_ROUTE_TC, st);   // the kinds in route order
 }
 
 thread_local char g_err[512];
@@ -690,7 +842,7 @@ int32_t lq_gemm_i8_route(int32_t batch, int32_t K, int32_t N) {
   using namespace lq::w8;
   if (batch < 1 || N < 1 || K < 1 || K > LQ_MAX_I8_K || batch > kMost || N > kMost) return -1;
   if (few_tokens(batch, K, N)) return LQ_I8_ROUTE_GEMV;
-  return make_plan(batch, K, N, 148).pair ? LQ_I8_ROUTE_PAIR : LQ_I8_ROUTE_TC;
+  return LQ_I8_ROUTE_TC + make_plan(batch, K, N, 148).kind;
 }
 
 lq_status lq_gemm_i8(const int8_t* xq, const float* xs, int32_t batch, const int8_t* wq,
@@ -708,7 +860,7 @@ lq_status lq_gemm_i8(const int8_t* xq, const float* xs, int32_t batch, const int
     return reject(LQ_EUNSUPPORTED, "lq_gemm_i8: batch = %d or N = %d exceeds %d", batch, N, kMost);
   if (ydt != LQ_F32 && ydt != LQ_F16 && ydt != LQ_BF16)
     return reject(LQ_EINVAL, "lq_gemm_i8: unknown y dtype %d", (int)ydt);
-  if (route < -1 || route > LQ_I8_ROUTE_PAIR)
+  if (route < -1 || route > LQ_I8_ROUTE_SPLIT)
     return reject(LQ_EINVAL, "lq_gemm_i8: unknown route %d", route);
   if (route == LQ_I8_ROUTE_GEMV && batch > LQ_I8_GEMV_MAX_BATCH)
     return reject(LQ_EUNSUPPORTED, "lq_gemm_i8: %d tokens on the GEMV route (at most %d)", batch,

@@ -354,6 +354,7 @@ LQ_API lq_status lq_norm_residual(const void* h, lq_dtype hdt, int64_t ldh, cons
 #define LQ_I8_ROUTE_GEMV 0  /* warp-level int8 MMA, up to LQ_I8_GEMV_MAX_BATCH tokens */
 #define LQ_I8_ROUTE_TC 1    /* tcgen05 kind::i8 tiles, any batch */
 #define LQ_I8_ROUTE_PAIR 2  /* the same tiles by pairs of CTAs, any batch */
+#define LQ_I8_ROUTE_SPLIT 3 /* the same tiles by clusters that split K, any batch */
 #define LQ_I8_GEMV_MAX_BATCH 16
 /* Bytes of the lq_gemm_i8 workspace: the status word. */
 #define LQ_GEMM_I8_WORKSPACE_BYTES 256

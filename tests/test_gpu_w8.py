@@ -217,13 +217,23 @@ def test_gemm_small_batches_on_both_routes(batch, K, N, route):
                                        (33, 2048, 1000), (64, 4100, 515), (100, 128, 30),
                                        (129, 1000, 2050), (256, 512, 512), (257, 384, 770),
                                        (700, 640, 5001), (1025, 200, 300), (300, 2056, 19000)])
-@pytest.mark.parametrize("route", [lq.I8_ROUTE_TC, lq.I8_ROUTE_PAIR])
+@pytest.mark.parametrize("route", [lq.I8_ROUTE_TC, lq.I8_ROUTE_PAIR, lq.I8_ROUTE_SPLIT])
 def test_gemm_tile_kernels(batch, K, N, route):
     check_gemm(batch, K, N, BF16, False, route=route)
     check_gemm(batch, K, N, F32, True, route=route)
 
 
-@pytest.mark.parametrize("route", [lq.I8_ROUTE_TC, lq.I8_ROUTE_PAIR])
+@pytest.mark.parametrize("batch,K,N", [(1, 14337, 64), (9, 15000, 130), (16, 20480, 1184),
+                                       (20, 8192, 1024), (40, 131071, 64), (85, 6912, 238),
+                                       (404, 5000, 441), (1000, 2048, 256), (19, 16752, 5218)])
+def test_gemm_by_clusters_along_k(batch, K, N):
+    """Layers of few tiles, which the library's own choice splits along K."""
+    assert lq.gemm_i8_route(batch, K, N) == lq.I8_ROUTE_SPLIT
+    for dtype in (BF16, F16, F32):
+        check_gemm(batch, K, N, dtype, dtype != F16)
+
+
+@pytest.mark.parametrize("route", [lq.I8_ROUTE_TC, lq.I8_ROUTE_PAIR, lq.I8_ROUTE_SPLIT])
 def test_gemm_tiles_with_odd_rows_of_y(route):
     """16-bit outputs at an odd width or off a 4-byte boundary are stored one by one."""
     check_gemm(70, 256, 333, F16, True, route=route)
@@ -288,7 +298,7 @@ def test_offsets_past_32_bits():
     del x, c, n
     batch, K, N = 70000, 64, 32768
     xq, wq, xs, sw = int8(batch, K, 1), int8(N, K, 2), scales(batch, 3), scales(N, 4)
-    for route in (lq.I8_ROUTE_TC, lq.I8_ROUTE_PAIR):
+    for route in (lq.I8_ROUTE_TC, lq.I8_ROUTE_PAIR, lq.I8_ROUTE_SPLIT):
         y = lq.gemm_i8(xq, xs, wq, sw, dtype=BF16, route=route)
         ref.within(y[-5:], *ref.product(xq[-5:], xs[-5:], wq, sw, K, None))
         ref.within(y[:5], *ref.product(xq[:5], xs[:5], wq, sw, K, None))
@@ -313,6 +323,7 @@ def test_gemm_same_bits_every_time():
         if batch <= 16:     # the integer sum does not depend on the kernel
             assert torch.equal(y, lq.gemm_i8(xq, xs, wq, sw, route=lq.I8_ROUTE_TC))
         assert torch.equal(y, lq.gemm_i8(xq, xs, wq, sw, route=lq.I8_ROUTE_PAIR))
+        assert torch.equal(y, lq.gemm_i8(xq, xs, wq, sw, route=lq.I8_ROUTE_SPLIT))
 
 
 def test_graphs_share_a_workspace():

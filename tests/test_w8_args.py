@@ -32,6 +32,11 @@ def test_routes(L):
     assert lq.gemm_i8_route(16, 4096, 4096) == lq.I8_ROUTE_GEMV
     assert lq.gemm_i8_route(16, 8192, 28672) in (lq.I8_ROUTE_TC, lq.I8_ROUTE_PAIR)
     assert lq.gemm_i8_route(17, 64, 64) == lq.I8_ROUTE_TC
+    assert lq.gemm_i8_route(20, 28672, 1024) == lq.I8_ROUTE_SPLIT
+    assert lq.gemm_i8_route(1, 28672, 1024) == lq.I8_ROUTE_SPLIT
+    assert lq.gemm_i8_route(1, 14336, 1024) == lq.I8_ROUTE_GEMV
+    assert lq.gemm_i8_route(2**30, 64, 64) == lq.I8_ROUTE_TC
+    assert lq.gemm_i8_route(2**30, 64, 2**30) in (lq.I8_ROUTE_TC, lq.I8_ROUTE_PAIR)
     for bad in ((0, 64, 64), (1, 0, 64), (1, 64, 0), (1, 131072, 64), (2 ** 30 + 1, 64, 64),
                 (1, 64, 2 ** 30 + 1)):
         assert lq.gemm_i8_route(*bad) == -1
@@ -98,7 +103,7 @@ def gemm(L, **kw):
 
 def test_gemm_arguments(L):
     for kw in (dict(xq=None), dict(xs=None), dict(wq=None), dict(ws=None), dict(y=None),
-               dict(w=None), dict(batch=-1), dict(N=-1), dict(K=0), dict(dt=3), dict(route=3),
+               dict(w=None), dict(batch=-1), dict(N=-1), dict(K=0), dict(dt=3), dict(route=4),
                dict(route=-2), dict(xq=FAKE + 8), dict(wq=FAKE + 4), dict(xs=FAKE + 2),
                dict(ws=FAKE + 1), dict(b=FAKE + 2), dict(y=FAKE + 2), dict(y=FAKE + 1, dt=2),
                dict(w=FAKE + 128), dict(wb=255)):
