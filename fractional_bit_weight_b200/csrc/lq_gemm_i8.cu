@@ -11,8 +11,7 @@
 //    16 consecutive bytes of its row and of its token and feeds them as the operand words of two
 //    MMAs: no shuffles and no shared memory on the way in. One CTA takes sixteen rows, its warps
 //    take turns over K; their int32 partials meet in shared memory. Measured (device): one token
-//    8192 -> 28672 40.2 us, 5.85 TB/s, 0.89 of the copy rate (47.6 with eight warps to every CTA,
-//    three waves of them); 28672 -> 8192 37.1 us (0.97); 4096 -> 4096 3.6 us.
+//    28672 -> 8192 36.4 us, 6.45 TB/s, 0.98 of the copy rate; 4096 -> 4096 3.6 us.
 //  * gemm_w8_kernel (any batch): persistent tcgen05.mma kind::i8 over tiles of up to 128 rows x 256
 //    tokens (256 x 256 by a pair of CTAs) with two int32 accumulators in tensor memory, operands
 //    brought by TMA. The weights are the lanes of the accumulator, so the token tile fits the batch
@@ -693,8 +692,12 @@ Plan make_plan(int batch, int K, int N, int sms, int force = -1) {
   for (int kind : {kOne, kPair}) {
     if (force >= 0 && kind != force) continue;
     const int ctas = kind == kPair ? 2 : 1, units = sms / ctas, unit = 16 * ctas;
+    // Small layers like small tiles: with ten against four counts of token tiles 1024 x 1024 x 1024
+    // takes 5.9 against 8.5 us, 2048 x 4096 x 1024 13.7 against 15.9. Pairs of fewer tokens lose to
+    // the estimate under the power limit: 1504 x 8624 x 3284 55 us at 192 tokens, 63 at 160.
+    const int counts = kind == kPair ? 4 : 10;
     int last = 0;
-    for (int tiles_t = (batch + kMaxTokens - 1) / kMaxTokens, tries = 0; tries < 4; ++tiles_t, ++tries) {
+    for (int tiles_t = (batch + kMaxTokens - 1) / kMaxTokens, tries = 0; tries < counts; ++tiles_t, ++tries) {
       const int tokens = ((batch + tiles_t - 1) / tiles_t + unit - 1) / unit * unit;
       if (tokens == last) continue;
       last = tokens;
@@ -806,10 +809,15 @@ cudaError_t launch_tc(const Args& a, int force, cudaStream_t st) {
 // 14336 x 4096, 15.0 against 14.3 on 8192 x 8192 and 43.3 against 38.7 us on 28672 x 8192. With a
 // CTA per 16 rows it leaves half the SMs idle on a layer of up to 1184 rows, where clusters along K
 // win on long ones: at one token 3.8 against 5.1 us on 8192 x 1024, 6.1 against 6.1 us on 14336 x
-// 1024, 12.5 against 8.6 us on 28672 x 1024.
+// 1024, 12.5 against 8.6 us on 28672 x 1024. On layers that give it more CTAs than are resident at
+// once, the persistent tiles lose nothing between them: at one token 36.4 against 38.4 us on 28672 x
+// 8192 and 23.0 against 23.6 on 8192 x 16384, but 41.7 against 38.6 on 8192 x 28672 and 78.2 against
+// 71.8 on 8192 x 57344; not with rows of 4096 (20.0 against 20.4 us on 28672 of them).
 bool few_tokens(int32_t batch, int32_t K, int32_t N) {
+  const int64_t weights = (int64_t)N * K;
   if (batch > LQ_I8_GEMV_MAX_BATCH || (N <= 16 * 74 && K > 14336)) return false;
-  return batch <= 8 || (int64_t)N * K <= 54 * 1000 * 1000;
+  if (N > 16384 && K >= 8192 && weights > 200 * 1000 * 1000) return false;
+  return batch <= 8 || weights <= 54 * 1000 * 1000;
 }
 
 cudaError_t launch(const Args& a, int route, cudaStream_t st) {

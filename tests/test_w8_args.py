@@ -28,7 +28,8 @@ def test_routes(L):
     assert lq.gemm_i8_route(1, 4096, 4096) == lq.I8_ROUTE_GEMV
     assert lq.gemm_i8_route(2048, 8192, 28672) == lq.I8_ROUTE_PAIR
     assert lq.gemm_i8_route(128, 4096, 4096) == lq.I8_ROUTE_TC
-    assert lq.gemm_i8_route(8, 8192, 28672) == lq.I8_ROUTE_GEMV
+    assert lq.gemm_i8_route(8, 28672, 8192) == lq.I8_ROUTE_GEMV
+    assert lq.gemm_i8_route(1, 8192, 28672) in (lq.I8_ROUTE_TC, lq.I8_ROUTE_PAIR)
     assert lq.gemm_i8_route(16, 4096, 4096) == lq.I8_ROUTE_GEMV
     assert lq.gemm_i8_route(16, 8192, 28672) in (lq.I8_ROUTE_TC, lq.I8_ROUTE_PAIR)
     assert lq.gemm_i8_route(17, 64, 64) == lq.I8_ROUTE_TC
