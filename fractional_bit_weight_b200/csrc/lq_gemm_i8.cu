@@ -649,9 +649,9 @@ constexpr int32_t kMost = 1 << 30;          // tokens, rows: tile coordinates st
 
 // The tile of a call. Rows of a tile are chosen so that its tiles fill whole waves of the SMs: few
 // rows cost nothing while the weights' stream bounds the call, and no K is split. Token tiles,
-// CTA pairs and rows are compared by an estimate in clocks, fitted to a sweep of tiles over 24 to
-// 4096 tokens and layers of 1024 x 4224 to 8192 x 28672 (the tile it picks was within 2 % of the
-// fastest on average, 9 % at worst): per 128 inputs the MMAs (2 clocks per token), the operands'
+// CTA pairs and rows are compared by an estimate in clocks, fitted to sweeps of tiles (over 13 layers
+// of 1024 x 1024 to 8192 x 28672 with 17 batches of 20 to 4096 tokens the tile it picks is within
+// 1.1 % of the fastest on average, 4 % in nine of ten, 19 % at worst): per 128 inputs the MMAs (2 clocks per token), the operands'
 // way into and out of shared memory (0.82 clocks per 128-byte row) or the rows fetched through L2
 // (1.67 clocks each), whichever is longest; per wave 6000; for the last epilogue 33 per token; for
 // a pair's start 4800. Pairs: 2048 x 8192 x 28672 308 against 344 us, 128 x 4096 x 4096 10.2

@@ -14,8 +14,8 @@
 // instructions per entry (about 25 for two norms and a gate, 27 for whitened codes with their
 // values) do; the latency of load -> reductions -> store for a few. Measured (device, us and share
 // of the 6551 GB/s copy rate): codes of 8192 x 8192 fp32 91 (1.01), of 2048 x 28672 bf16 whitened
-// in blocks of 256 with values 75 (0.60; issue slots 65 % busy), of 4 x 8192 3.0; two norms, gate
-// and residual on 2048 x 8192 31 (0.83), on one row of 8192 4.0.
+// in blocks of 256 with values 70 (0.64; issue slots 63 % busy), of 4 x 8192 2.9; two norms, gate
+// and residual on 2048 x 8192 30.5 (0.84), on one row of 8192 3.9.
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
