@@ -648,22 +648,19 @@ constexpr int kSplitFit[] = {0, 148, 74, 0, 33, 0, 0, 0, 15};   // clusters of 2
 constexpr int32_t kMost = 1 << 30;          // tokens, rows: tile coordinates stay in 32 bits
 
 // The tile of a call. Rows of a tile are chosen so that its tiles fill whole waves of the SMs: few
-// rows cost nothing while the weights' stream bounds the call, and no K is split. Token tiles,
-// CTA pairs and rows are compared by an estimate in clocks, fitted to sweeps of tiles (over 13 layers
-// of 1024 x 1024 to 8192 x 28672 with 17 batches of 20 to 4096 tokens the tile it picks is within
-// 1.1 % of the fastest on average, 4 % in nine of ten, 19 % at worst): per 128 inputs the MMAs (2 clocks per token), the operands'
-// way into and out of shared memory (0.82 clocks per 128-byte row) or the rows fetched through L2
-// (1.67 clocks each), whichever is longest; per wave 6000; for the last epilogue 33 per token; for
-// a pair's start 4800. Pairs: 2048 x 8192 x 28672 308 against 344 us, 128 x 4096 x 4096 10.2
-// against 9.7 us.
+// rows cost nothing while the weights' stream bounds the call. Token tiles, rows, CTA pairs and
+// clusters along K are compared by an estimate in clocks: per 128 inputs 1.22 for each 128-byte row
+// that an SM fetches into shared memory or reads out of it for the MMAs (those take 2 per token, less
+// than that); per wave 5050; for the last epilogue 39 per token; for a pair's start 2600. It is
+// fitted to sweeps of all tiles over 13 layers of 1024 x 1024 to 8192 x 28672 with 17 batches of 20
+// to 4096 tokens: the tile it picks is within 1.0 % of the fastest on average, 4 % in nine of ten,
+// 15 % at worst. Pairs against single CTAs: 2048 x 8192 x 28672 293 against 344 us, 256 x 5120 x 5120
+// 13.2 against 14.5; and 128 x 4096 x 4096 10.2 against 8.2, 32 x 8192 x 8192 15.4 against 15.0.
 //
 // Clusters along K are taken while they are all resident at once: the sixteenth cluster of 8 waits
-// for the first (15 of them 8.2 us, 16 14.6), as the 34th of 4 does (33 10.9, 34 19.1). Their
-// estimate is fitted to 51 layers of 128 to 8192 rows with 16 to 2000 tokens (the tile picked was
-// within 1.2 % of the fastest on average, 9 % at worst). Split against whole: 32 x 8192 x 1024 6.3
-// against 9.9 us, 20 x 28672 x 1024 10.0 against 26.4, 64 x 14336 x 4096 15.2 against 18.9, 512 x
-// 4096 x 1024 9.2 against 11.3; and 24 x 1024 x 1024 4.3 against 3.5, 64 x 8192 x 8192 16.5
-// against 15.8.
+// for the first (15 of them 8.2 us, 16 14.6), as the 34th of 4 does (33 10.9, 34 19.1). Split
+// against whole: 32 x 8192 x 1024 5.9 against 9.6 us, 20 x 28672 x 1024 9.2 against 26.1, 64 x 14336
+// x 4096 14.9 against 18.5; and 24 x 1024 x 1024 4.3 against 3.5, 64 x 8192 x 8192 16.5 against 15.8.
 Plan make_plan(int batch, int K, int N, int sms, int force = -1) {
   Plan best{};
   double best_cost = 0;
@@ -671,15 +668,13 @@ Plan make_plan(int batch, int K, int N, int sms, int force = -1) {
   auto consider = [&](int kind, int split, int rows, int tokens, int64_t tn, int tt, int64_t waves) {
     const int shared = kind == kPair ? 2 : 1;          // CTAs that share a tile's tokens
     const int fetched = rows + tokens / shared;
-    const double mma = std::max(160.0, 2.0 * tokens);
-    const double smem = 0.82 * (kMmaM + tokens / shared + fetched);
-    const double step = std::max({mma, smem, 1.67 * fetched});
+    const double step = 1.22 * (kMmaM + tokens / shared + fetched);
     double cost;
     if (kind == kSplit)
-      cost = (double)waves * (1.36 * ((chunks_k + split - 1) / split) * step + 53.0 * tokens +
-                              35.0 * tokens / split + 7070);
+      cost = (double)waves * (1.4 * ((chunks_k + split - 1) / split) * step + 55.0 * tokens +
+                              27.0 * tokens / split + 7000);
     else
-      cost = (double)waves * (chunks_k * step + 6000) + 33.0 * tokens + (kind == kPair ? 4800.0 : 0.0);
+      cost = (double)waves * (chunks_k * step + 5050) + 39.0 * tokens + (kind == kPair ? 2600.0 : 0.0);
     if (best.tokens != 0 && cost >= best_cost) return;
     best_cost = cost;
     best.kind = kind;
@@ -693,11 +688,9 @@ Plan make_plan(int batch, int K, int N, int sms, int force = -1) {
     if (force >= 0 && kind != force) continue;
     const int ctas = kind == kPair ? 2 : 1, units = sms / ctas, unit = 16 * ctas;
     // Small layers like small tiles: with ten against four counts of token tiles 1024 x 1024 x 1024
-    // takes 5.9 against 8.5 us, 2048 x 4096 x 1024 13.7 against 15.9. Pairs of fewer tokens lose to
-    // the estimate under the power limit: 1504 x 8624 x 3284 55 us at 192 tokens, 63 at 160.
-    const int counts = kind == kPair ? 4 : 10;
+    // takes 5.9 against 8.5 us, 400 x 17792 x 1364 20.1 against 26.6.
     int last = 0;
-    for (int tiles_t = (batch + kMaxTokens - 1) / kMaxTokens, tries = 0; tries < counts; ++tiles_t, ++tries) {
+    for (int tiles_t = (batch + kMaxTokens - 1) / kMaxTokens, tries = 0; tries < 10; ++tiles_t, ++tries) {
       const int tokens = ((batch + tiles_t - 1) / tiles_t + unit - 1) / unit * unit;
       if (tokens == last) continue;
       last = tokens;
