@@ -17,7 +17,7 @@ __all__ = [
     "new_workspace",
     "device_status", "check_wait_timeout", "NOALLOC_SCRATCH_BYTES",
     "i8_row_bytes", "quant_i8", "Norm", "norm_residual", "norm_residual_i8", "gemm_i8",
-    "gemm_i8_route", "new_i8_workspace", "GEMM_I8_WORKSPACE_BYTES",
+    "gemm_i8_route", "gemm_i8_plan", "new_i8_workspace", "GEMM_I8_WORKSPACE_BYTES",
 ]
 
 NOALLOC_SCRATCH_BYTES = 8 << 20   # LQ_NOALLOC_SCRATCH_BYTES
@@ -33,7 +33,8 @@ EXPORTS = ("lq_abi_version", "lq_lifted_bits", "lq_row_stride_bytes", "lq_pack",
            "lq_whiten", "lq_lift", "lq_gemm_workspace_bytes", "lq_gemm_launches", "lq_gemm_route",
            "lq_gemm", "lq_gemm_on_route", "lq_gemm_route_workspace_bytes", "lq_gemv_staged_plan",
            "lq_codebook_workspace_bytes", "lq_codebook_round",
-           "lq_i8_row_bytes", "lq_quant_i8", "lq_norm_residual", "lq_gemm_i8_route", "lq_gemm_i8",
+           "lq_i8_row_bytes", "lq_quant_i8", "lq_norm_residual", "lq_gemm_i8_route", "lq_gemm_i8_plan",
+           "lq_gemm_i8",
            "lq_gemm_noalloc", "lq_check_wait_timeout",
            "lq_device_status", "lq_status_string", "lq_last_error")
 
@@ -95,6 +96,7 @@ def _declare(L):
                               ctypes.c_float, vp, ctypes.POINTER(NormDesc), vp, ctypes.c_int, dp,
                               vp, vp, vp], ctypes.c_int),
         "lq_gemm_i8_route": ([i32, i32, i32], i32),
+        "lq_gemm_i8_plan": ([i32, i32, i32, i32, ctypes.POINTER(i64)], ctypes.c_int),
         "lq_gemm_i8": ([vp, vp, i32, vp, vp, vp, i32, i32, vp, ctypes.c_int, vp, sz, i32, vp],
                        ctypes.c_int),
         "lq_device_status": ([vp, ctypes.POINTER(i32), vp], ctypes.c_int),
@@ -596,6 +598,17 @@ def norm_residual_i8(h, residual=None, post=None, pre=None, gate=None, gate_toke
 def gemm_i8_route(batch, K, N):
     """Which kernel lq_gemm_i8 runs for this shape (host-only query; I8_ROUTE_* codes)."""
     return int(lib().lq_gemm_i8_route(batch, K, N))
+
+
+I8_PLAN_FIELDS = ("route", "cluster", "tiles", "rows", "tokens", "chunks", "stages", "smem")
+
+
+def gemm_i8_plan(batch, K, N, route=None):
+    """The tiles of lq_gemm_i8's tensor-core routes for a shape (host-only query), as a dict."""
+    out = (ctypes.c_int64 * len(I8_PLAN_FIELDS))()
+    _check(lib().lq_gemm_i8_plan(batch, K, N, -1 if route is None else route, out),
+           "lq_gemm_i8_plan")
+    return dict(zip(I8_PLAN_FIELDS, (int(v) for v in out)))
 
 
 def new_i8_workspace(device="cuda"):

@@ -24,7 +24,8 @@
 //    -> 1024 5.9 us (9.6 unsplit), 20 tokens 28672 -> 1024 9.2 us (26.1).
 // Every wait on an mbarrier is bounded in time: on expiry the kernel records LQ_ETIMEOUT in the
 // workspace status word, the roles leave their loops, in-flight copies and MMAs are waited for
-// (again bounded) and tensor memory is released before the CTA exits.
+// (again bounded) and tensor memory is released before the CTA exits. tcgen05.alloc has no limit of
+// its own; the shared memory of clusters (kAloneSmem) keeps it from waiting for ever.
 #include <cuda.h>
 
 #include <cstdarg>
@@ -641,6 +642,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ------------------------------------------------------------------ host side
 
 constexpr size_t kMaxSmem = 227 * 1024;
+// More than half of what an SM has (228 KB, 1 KB of it taken by each CTA): two CTAs of this size
+// never share one. A CTA of a cluster keeps its tensor memory until its peers have allocated theirs.
+// If CTAs of clusters X and Y shared two SMs, X's could hold one and wait for the other while Y's did
+// the reverse, and tcgen05.alloc waits without a limit. So every cluster asks for this much. A CTA
+// without a cluster waits for no other with its tensor memory held, so it may share an SM with any.
+constexpr size_t kAloneSmem = kMaxSmem / 2 + 1024;
 constexpr int kMaxSplit = 8;                // CTAs of a cluster along K
 constexpr int kSplitTokens = 128;           // tokens of a kSplit tile: its partials fit the ring
 constexpr int kSplitFit[] = {0, 148, 74, 0, 33, 0, 0, 0, 15};   // clusters of 2, 4 and 8 CTAs that
@@ -738,6 +745,7 @@ Plan make_plan(int batch, int K, int N, int sms, int force = -1) {
   if (best.kind == kSplit)   // the partials take the ring's place
     ring = std::max(ring, (size_t)best.split * best.cols * kMmaM * sizeof(int));
   best.smem = fixed + ring;
+  if (best.kind != kOne) best.smem = std::max(best.smem, kAloneSmem);
   return best;
 }
 
@@ -844,6 +852,22 @@ int32_t lq_gemm_i8_route(int32_t batch, int32_t K, int32_t N) {
   if (batch < 1 || N < 1 || K < 1 || K > LQ_MAX_I8_K || batch > kMost || N > kMost) return -1;
   if (few_tokens(batch, K, N)) return LQ_I8_ROUTE_GEMV;
   return LQ_I8_ROUTE_TC + make_plan(batch, K, N, 148).kind;
+}
+
+lq_status lq_gemm_i8_plan(int32_t batch, int32_t K, int32_t N, int32_t route, int64_t* out) {
+  using namespace lq::w8;
+  lq::set_last_error("%s", "");
+  if (!out) return reject(LQ_EINVAL, "lq_gemm_i8_plan: null out");
+  if (lq_gemm_i8_route(batch, K, N) < 0)
+    return reject(LQ_EINVAL, "lq_gemm_i8_plan: invalid sizes batch=%d K=%d N=%d", batch, K, N);
+  if (route != -1 && (route < LQ_I8_ROUTE_TC || route > LQ_I8_ROUTE_SPLIT))
+    return reject(LQ_EINVAL, "lq_gemm_i8_plan: route %d has no tiles", route);
+  const Plan p = make_plan(batch, K, N, 148, route < 0 ? -1 : route - LQ_I8_ROUTE_TC);
+  const int64_t v[LQ_I8_PLAN_FIELDS] = {LQ_I8_ROUTE_TC + p.kind, p.kind == kPair ? 2 : p.split,
+                                        (int64_t)p.tiles_n * p.tiles_t, p.rows, p.tokens, p.chunks,
+                                        p.stages, (int64_t)p.smem};
+  for (int i = 0; i < LQ_I8_PLAN_FIELDS; ++i) out[i] = v[i];
+  return LQ_OK;
 }
 
 lq_status lq_gemm_i8(const int8_t* xq, const float* xs, int32_t batch, const int8_t* wq,

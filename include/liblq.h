@@ -363,6 +363,15 @@ LQ_API lq_status lq_norm_residual(const void* h, lq_dtype hdt, int64_t ldh, cons
  * invalid sizes. */
 LQ_API int32_t lq_gemm_i8_route(int32_t batch, int32_t K, int32_t N);
 
+/* The tiles of the tensor-core routes for this shape; route: -1 for the plan that the library
+ * compares its choice by, or one of LQ_I8_ROUTE_TC to LQ_I8_ROUTE_SPLIT. Host-only, touches no
+ * device: it lets tests check the plan's bounds. out[0 .. LQ_I8_PLAN_FIELDS) receives: the route,
+ * CTAs per cluster (1: none), tiles, weight rows per CTA and tokens of a tile, 128-byte chunks per
+ * stage, ring stages, dynamic shared memory (bytes).
+ * Errors: LQ_EINVAL on invalid sizes, a route without tiles or a null out. */
+#define LQ_I8_PLAN_FIELDS 8
+LQ_API lq_status lq_gemm_i8_plan(int32_t batch, int32_t K, int32_t N, int32_t route, int64_t* out);
+
 /* Matrix product in 8-bit integers with a scale per token and per output channel:
  *     y[t][n] = (sum_k xq[t][k] wq[n][k]) * (xs[t] * ws[n]) + bias[n]
  * The sum is an exact int32 (entries may be -128..127), scaled in fp32 and rounded to y's type
