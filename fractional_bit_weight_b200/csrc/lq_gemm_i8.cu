@@ -545,15 +545,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      // the copies still in flight land before the CTA leaves (a stage of which only one operand
-      // was asked for never completes: after an abort, a bounded wait)
-      if (rank == 0) {
-        for (uint32_t i = min(issued, (uint32_t)p.stages); i > 0; --i) {
+      // What still arrives at this CTA's barriers does so before it leaves: another CTA may have live
+      // barriers in the same place by then. Commits free the last stages in both CTAs of a pair, and
+      // a freed stage's copies have landed. After an abort nothing frees them: then the copies in
+      // flight are waited for (a stage of which only one operand was asked for never completes: a
+      // bounded wait).
+      const uint32_t last = min(issued, (uint32_t)p.stages);
+      bool freed = ok && weights;
+      for (uint32_t i = last; freed && i > 0; --i) {
+        const uint32_t c = issued - i;
+        freed = wait_phase(&ctl->empty[c % p.stages], (c / p.stages) & 1, abort, true);
+        if (!freed) give_up(ctl, a.status);
+      }
+      if (rank == 0 && !freed) {
+        for (uint32_t i = last; i > 0; --i) {
           const uint32_t c = issued - i;
           if (!wait_phase(&ctl->full[c % p.stages], (c / p.stages) & 1, abort, false))
             give_up(ctl, a.status);
         }
       }
+      // the even CTA's last commit, which arrives here too
+      if (rank == 1 && weights && !wait_phase(&ctl->drain, 0, abort, false)) give_up(ctl, a.status);
     }
     __syncwarp();
   } else if (warp == kMmaWarp && rank == 0) {
