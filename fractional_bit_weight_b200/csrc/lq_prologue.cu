@@ -73,18 +73,6 @@ __global__ void lift_f32_kernel(const void* __restrict__ x, int xdt, int K, Whit
   }
 }
 
-cudaError_t ensure_smem(const void* func, size_t bytes, int* cache_per_device) {
-  if (bytes == 0) return cudaSuccess;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) dev = 0;
-  if (cache_per_device[dev] >= (int)bytes) return cudaSuccess;
-  e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (e == cudaSuccess) cache_per_device[dev] = (int)bytes;
-  return e;
-}
-
 cudaError_t launch_whiten(const void* x, int xdt, int32_t batch, int32_t K, Whiten T,
                           float* xt, cudaStream_t st) {
   if (batch == 0) return cudaSuccess;

@@ -1,4 +1,6 @@
 """Products in a row without a pause, where what one leaves behind could meet the next."""
+import threading
+
 import pytest
 import torch
 
@@ -64,4 +66,35 @@ def test_clusters_on_two_streams():
         torch.cuda.synchronize()
         for i, y in enumerate(got):
             assert torch.equal(y, want[i % 4])
+    assert lq.device_status(ws) == (lq.LQ_OK, 0)
+
+
+def test_two_host_threads():
+    """Calls of different shapes from two threads, each on its own stream."""
+    ws = lq.new_i8_workspace()
+    shapes = [[(2, 512, 300), (40, 256, 1000), (300, 1000, 4104), (33, 8192, 40)],
+              [(130, 128, 64), (16, 1000, 260), (20, 8192, 1024), (513, 256, 1030)]]
+    ops = [[operands(*s, seed=10 * t + i) for i, s in enumerate(shapes[t])] for t in range(2)]
+    torch.cuda.synchronize()
+    got, failed = [[], []], []
+
+    def work(t):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(10):
+                    got[t] = [lq.gemm_i8(*o, K=s[1], workspace=ws)
+                              for o, s in zip(ops[t], shapes[t])]
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:      # noqa: BLE001 (reported below, in the test's own thread)
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(t,)) for t in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+    for t in range(2):
+        for y, o, s in zip(got[t], ops[t], shapes[t]):
+            ref.within(y, *ref.product(*o, s[1], None))
     assert lq.device_status(ws) == (lq.LQ_OK, 0)
