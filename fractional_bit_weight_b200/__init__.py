@@ -454,31 +454,50 @@ def quant_i8(x, sign=None, chan_scale=None, block=0, values=False, stream=None):
     return (q, scale, v) if values else (q, scale)
 
 
+def _memory(t):
+    """What a descriptor depends on and what changes when a tensor's `.data` is replaced."""
+    return None if t is None else (t.data_ptr(), t.dtype, t.numel(), t.is_contiguous())
+
+
 class Norm:
     """A norm of lq_norm_residual: kind "rms" or "layer", weight and bias [K] (f32/f16/bf16, of
-    one type) or None, eps. Holds its tensors; make it once per layer."""
+    one type) or None, eps. Holds its tensors; make it once per layer. Each call takes the tensors
+    as they are then: they may have been given new storage or another type, or been replaced."""
 
     def __init__(self, kind, weight=None, bias=None, eps=1e-6):
-        if kind not in _NORM_KINDS:
-            raise ValueError(f"unknown norm kind {kind!r}, expected one of {sorted(_NORM_KINDS)}")
         self.kind, self.weight, self.bias, self.eps = kind, weight, bias, float(eps)
-        self.device = self.size = None
+        self._seen = None
+        self._look()
+
+    def _look(self):
+        """Makes the descriptor, after its checks, unless it was made of what is there now."""
+        try:
+            now = (self.kind, self.eps, _memory(self.weight), _memory(self.bias))
+        except AttributeError:      # not a tensor: refused below
+            now = None
+        if now is not None and now == self._seen:
+            return
+        if self.kind not in _NORM_KINDS:
+            raise ValueError(f"unknown norm kind {self.kind!r}, expected one of "
+                             f"{sorted(_NORM_KINDS)}")
+        device = size = None
         dtype = torch.float32
-        for t, name in ((weight, "weight"), (bias, "bias")):
+        address = {"weight": None, "bias": None}
+        for t, name in ((self.weight, "weight"), (self.bias, "bias")):
             if t is None:
                 continue
-            device = _device_of(t, name)
-            _arg(t, name, _DTYPES, device if self.device is None else self.device,
-                 (t.numel(),) if self.size is None else (self.size,))
-            if self.device is not None and t.dtype != dtype:
+            if device is not None and t.dtype != dtype:
                 raise TypeError("weight and bias of a norm must have one dtype")
-            self.device, self.size, dtype = device, t.numel(), t.dtype
-        self._desc = NormDesc(_NORM_KINDS[kind], self.eps,
-                              None if weight is None else weight.data_ptr(),
-                              None if bias is None else bias.data_ptr(), _DTYPES[dtype])
-        self._ref = ctypes.byref(self._desc)
+            address[name] = _arg(t, name, _DTYPES, _device_of(t, name) if device is None else device,
+                                 (t.numel(),) if size is None else (size,))
+            device, size, dtype = t.get_device(), t.numel(), t.dtype
+        # a new descriptor: another thread's call may be reading the last one
+        self._ref = ctypes.byref(NormDesc(_NORM_KINDS[self.kind], self.eps, address["weight"],
+                                          address["bias"], _DTYPES[dtype]))
+        self.device, self.size, self._seen = device, size, now
 
     def _arg(self, K, device):
+        self._look()
         if self.size is not None and (self.size != K or self.device != device):
             raise ValueError(f"norm over {self.size} entries on cuda:{self.device}, rows of {K} "
                              f"on cuda:{device}")

@@ -1,0 +1,35 @@
+"""Calls of the 8-bit and boundary operators that the other tests do not make."""
+import pytest
+import torch
+
+import fractional_bit_weight_b200 as lq
+import w8_ref as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
+
+
+def gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def rand(shape, dtype, g, scale=1.0):
+    return (scale * torch.randn(*shape, generator=g, device=DEV)).to(dtype)
+
+
+def test_norms_follow_their_tensors():
+    """A module that changes its type or is loaded anew keeps its Parameter objects."""
+    g = gen(1)
+    h = rand((5, 520), F32, g)
+    module = torch.nn.LayerNorm(520, device=DEV)
+    norm = lq.Norm("layer", module.weight, module.bias, 1e-5)
+    for dtype in (F32, BF16, F16, F32):
+        module.to(dtype)
+        for t in (module.weight, module.bias):
+            t.data = rand((520,), dtype, g)
+        got = lq.norm_residual(h, None, norm, norm, dtype=F32)[1]
+        fresh = lq.Norm("layer", module.weight, module.bias, 1e-5)
+        assert torch.equal(got, lq.norm_residual(h, None, fresh, fresh, dtype=F32)[1])
+        stats = ("layer", module.weight.detach(), module.bias.detach(), 1e-5)
+        ref.within(got, *ref.boundary(h, None, stats, stats, None, 1.0, 1.0)[2:])
