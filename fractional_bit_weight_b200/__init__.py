@@ -419,18 +419,28 @@ def _device_of(t, name):
     return t.get_device()
 
 
+_INT32_MAX = 2 ** 31 - 1
+
+
+def _int32(n, name):
+    """n, which ctypes would cut down to its low 32 bits without a word."""
+    if not -_INT32_MAX <= n <= _INT32_MAX:
+        raise ValueError(f"{name} = {n} exceeds 32 bits")
+    return n
+
+
 def _whiten_arg(sign, chan_scale, block, K, device):
     if not block:
         return None
     return ctypes.byref(WhitenDesc(
         None if sign is None else _arg(sign, "sign", _I8, device, (K,)),
         None if chan_scale is None else _arg(chan_scale, "chan_scale", _F32, device, (K,)),
-        int(block)))
+        _int32(int(block), "block")))
 
 
 def i8_row_bytes(K):
     """Bytes per row of int8 codes: K rounded up to a multiple of 16."""
-    return int(lib().lq_i8_row_bytes(K))
+    return int(lib().lq_i8_row_bytes(_int32(K, "K")))
 
 
 def quant_i8(x, sign=None, chan_scale=None, block=0, values=False, stream=None):
@@ -444,6 +454,7 @@ def quant_i8(x, sign=None, chan_scale=None, block=0, values=False, stream=None):
                            (x, sign, chan_scale))
     px, ldx = _rows(x, "x", _DTYPES, device)
     rows, K = x.shape
+    _int32(rows, "rows"), _int32(K, "K")
     q = x.new_empty((rows, (K + 15) // 16 * 16), dtype=torch.int8)
     scale = x.new_empty(rows, dtype=torch.float32)
     v = torch.empty_like(x, memory_format=torch.contiguous_format) if values else None
@@ -521,6 +532,7 @@ def _boundary(h, residual, post, pre, gate, gate_tokens, branch_scale, residual_
     device = h.get_device()
     ph, ldh = _rows(h, "h", _DTYPES, device)
     rows, K = shape = h.shape
+    _int32(rows, "rows"), _int32(K, "K")
     pr, ldr, rdt = None, 0, 0
     r_out = p_out = None
     if residual is not None:
@@ -547,7 +559,8 @@ def _boundary(h, residual, post, pre, gate, gate_tokens, branch_scale, residual_
         if tokens < 1 or count != max(1, -(-rows // tokens)):
             raise ValueError(f"gate of shape {tuple(gate.shape)} does not give {rows} tokens a "
                              f"row each {tokens}")
-        g = ctypes.byref(GateDesc(pg, _DTYPES[gate.dtype], cols, tokens))
+        g = ctypes.byref(GateDesc(pg, _DTYPES[gate.dtype], _int32(cols, "gate's columns"),
+                                  min(tokens, max(rows, 1))))
     n = q = scale = None
     if codes:
         q = h.new_empty((rows, (K + 15) // 16 * 16), dtype=torch.int8)
@@ -614,9 +627,13 @@ def norm_residual_i8(h, residual=None, post=None, pre=None, gate=None, gate_toke
     return (r, q, scale) if dtype is None else (r, q, scale, n)
 
 
+def _sizes(batch, K, N):
+    return _int32(batch, "batch"), _int32(K, "K"), _int32(N, "N")
+
+
 def gemm_i8_route(batch, K, N):
     """Which kernel lq_gemm_i8 runs for this shape (host-only query; I8_ROUTE_* codes)."""
-    return int(lib().lq_gemm_i8_route(batch, K, N))
+    return int(lib().lq_gemm_i8_route(*_sizes(batch, K, N)))
 
 
 I8_PLAN_FIELDS = ("route", "cluster", "tiles", "rows", "tokens", "chunks", "stages", "smem")
@@ -625,7 +642,8 @@ I8_PLAN_FIELDS = ("route", "cluster", "tiles", "rows", "tokens", "chunks", "stag
 def gemm_i8_plan(batch, K, N, route=None):
     """The tiles of lq_gemm_i8's tensor-core routes for a shape (host-only query), as a dict."""
     out = (ctypes.c_int64 * len(I8_PLAN_FIELDS))()
-    _check(lib().lq_gemm_i8_plan(batch, K, N, -1 if route is None else route, out),
+    _check(lib().lq_gemm_i8_plan(*_sizes(batch, K, N),
+                                 -1 if route is None else _int32(route, "route"), out),
            "lq_gemm_i8_plan")
     return dict(zip(I8_PLAN_FIELDS, (int(v) for v in out)))
 
@@ -655,6 +673,7 @@ def gemm_i8(xq, xs, wq, ws, K=None, bias=None, dtype=torch.float32, y=None, work
         K = row
     if (K + 15) // 16 * 16 != row:
         raise ValueError(f"rows of {row} bytes, {(K + 15) // 16 * 16} expected for K = {K}")
+    _sizes(batch, K, N)
     pxq = _arg(xq, "xq", _I8, device)
     pwq = _arg(wq, "wq", _I8, device, (N, row))
     pxs = _arg(xs, "xs", _F32, device, (batch,))
@@ -670,7 +689,7 @@ def gemm_i8(xq, xs, wq, ws, K=None, bias=None, dtype=torch.float32, y=None, work
         workspace = new_i8_workspace(xq.device)
     pw = _arg(workspace, "workspace", (torch.uint8,), device)
     _check(lib().lq_gemm_i8(pxq, pxs, batch, pwq, pws, pb, K, N, y.data_ptr(), _DTYPES[y.dtype],
-                            pw, workspace.numel(), -1 if route is None else route,
+                            pw, workspace.numel(), -1 if route is None else _int32(route, "route"),
                             _raw_stream(device)), "lq_gemm_i8")
     return y
 

@@ -1,0 +1,89 @@
+"""What the binding of the 8-bit and boundary operators passes on, refuses and keeps. No GPU is
+used: host and meta tensors stand in for the device's, and a recorder for the library."""
+import ctypes
+
+import pytest
+import torch
+
+import fractional_bit_weight_b200 as lq
+
+HOST = -1                   # get_device() of a host or meta tensor
+HUGE = 2 ** 32 + 4          # its low 32 bits are a small number
+
+
+class Recorder:
+    """Every entry point returns LQ_OK and leaves its arguments in calls."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append((name, args))
+            return 0
+        return call
+
+
+@pytest.fixture
+def rec(monkeypatch):
+    r = Recorder()
+    monkeypatch.setattr(lq, "lib", lambda: r)
+    monkeypatch.setattr(lq, "_device_of", lambda t, name: t.get_device())
+    monkeypatch.setattr(lq, "_current_device", lambda: HOST)
+    monkeypatch.setattr(lq, "_raw_stream", lambda device: 0)
+    return r
+
+
+def descriptor(call, kind):
+    """The descriptor of this kind among a call's arguments."""
+    return next(a._obj for a in call[1] if isinstance(getattr(a, "_obj", None), kind))
+
+
+def meta(*shape, dtype=torch.float32):
+    return torch.empty(*shape, dtype=dtype, device="meta")
+
+
+def test_sizes_past_32_bits_are_refused(rec):
+    i8 = torch.int8
+    ws = torch.zeros(256, dtype=torch.uint8)
+    calls = [lambda: lq.quant_i8(meta(HUGE, 1)), lambda: lq.quant_i8(meta(1, HUGE)),
+             lambda: lq.norm_residual(meta(HUGE, 1)), lambda: lq.norm_residual_i8(meta(1, HUGE)),
+             lambda: lq.gemm_i8(meta(HUGE, 16, dtype=i8), meta(HUGE), meta(4, 16, dtype=i8), meta(4),
+                                workspace=ws),
+             lambda: lq.gemm_i8(meta(4, 16, dtype=i8), meta(4), meta(HUGE, 16, dtype=i8), meta(HUGE),
+                                workspace=ws),
+             lambda: lq.gemm_i8(meta(1, 2 ** 32 + 16, dtype=i8), meta(1),
+                                meta(1, 2 ** 32 + 16, dtype=i8), meta(1), workspace=ws),
+             lambda: lq.gemm_i8(meta(4, 16, dtype=i8), meta(4), meta(4, 16, dtype=i8), meta(4),
+                                workspace=ws, route=2 ** 32),
+             lambda: lq.quant_i8(meta(4, 512), block=2 ** 32 + 256),
+             lambda: lq.norm_residual(meta(4, 64), gate=meta(1, 2 ** 32 + 64)),
+             lambda: lq.i8_row_bytes(HUGE), lambda: lq.gemm_i8_route(HUGE, 64, 64),
+             lambda: lq.gemm_i8_plan(4, HUGE, 64), lambda: lq.gemm_i8_plan(4, 64, 64, 2 ** 32 + 1)]
+    for call in calls:
+        with pytest.raises(ValueError, match="exceeds 32 bits"):
+            call()
+    assert not rec.calls
+
+
+@pytest.mark.parametrize("gate_tokens", [8, 100, 2 ** 31, 2 ** 32 + 1, 2 ** 40])
+def test_one_gate_row_for_any_number_of_tokens(rec, gate_tokens):
+    """Cut down to 32 bits, 2^32 + 1 would send token t to row t of a gate of one row."""
+    h, gate = torch.zeros(8, 64), torch.zeros(1, 64)
+    lq.norm_residual(h, gate=gate, gate_tokens=gate_tokens)
+    d = descriptor(rec.calls[-1], lq.GateDesc)
+    assert d.cols == 64 and d.gate == gate.data_ptr()
+    assert all(t // d.tokens == 0 for t in range(8))
+
+
+def test_gate_rows(rec):
+    h = torch.zeros(8, 64)
+    for shape, given, tokens in (((64,), 0, 8), ((1, 64), 0, 8), ((8, 64), 0, 1), ((8, 1), 0, 1),
+                                 ((3, 64), 3, 3), ((2, 1), 7, 7)):
+        lq.norm_residual(h, gate=torch.zeros(shape), gate_tokens=given)
+        d = descriptor(rec.calls[-1], lq.GateDesc)
+        assert (d.tokens, d.cols) == (tokens, shape[-1])
+    for shape, given in (((2, 64), 0), ((9, 64), 1), ((3, 64), 4), ((1, 64), -1)):
+        with pytest.raises(ValueError, match="does not give"):
+            lq.norm_residual(h, gate=torch.zeros(shape), gate_tokens=given)
+    assert ctypes.sizeof(lq.GateDesc) == 24
