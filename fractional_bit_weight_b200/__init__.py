@@ -556,7 +556,8 @@ def _boundary(h, residual, post, pre, gate, gate_tokens, branch_scale, residual_
         cols = gate.shape[-1] if gate.dim() == 2 else gate.numel()
         count = gate.numel() // cols if cols else 0
         tokens = int(gate_tokens) or (1 if count == rows else max(rows, 1))
-        if tokens < 1 or count != max(1, -(-rows // tokens)):
+        # no tokens: no row of the gate is read, be there none or one for all
+        if tokens < 1 or count != -(-rows // tokens) and (rows or count != 1):
             raise ValueError(f"gate of shape {tuple(gate.shape)} does not give {rows} tokens a "
                              f"row each {tokens}")
         g = ctypes.byref(GateDesc(pg, _DTYPES[gate.dtype], _int32(cols, "gate's columns"),

@@ -33,3 +33,13 @@ def test_norms_follow_their_tensors():
         assert torch.equal(got, lq.norm_residual(h, None, fresh, fresh, dtype=F32)[1])
         stats = ("layer", module.weight.detach(), module.bias.detach(), 1e-5)
         ref.within(got, *ref.boundary(h, None, stats, stats, None, 1.0, 1.0)[2:])
+
+
+def test_boundary_of_an_empty_batch():
+    h = torch.empty(0, 64, device=DEV)
+    for gate, tokens in ((torch.empty(0, 64, device=DEV), 0), (torch.empty(0, 1, device=DEV), 5),
+                         (torch.ones(64, device=DEV), 0)):
+        c, n = lq.norm_residual(h, h, None, lq.Norm("rms"), gate, tokens)
+        assert c.shape == n.shape == (0, 64)
+        c, q, s = lq.norm_residual_i8(h, h, None, None, gate, tokens, block=64)
+        assert q.shape == (0, 64) and s.shape == (0,)

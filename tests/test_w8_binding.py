@@ -87,3 +87,14 @@ def test_gate_rows(rec):
         with pytest.raises(ValueError, match="does not give"):
             lq.norm_residual(h, gate=torch.zeros(shape), gate_tokens=given)
     assert ctypes.sizeof(lq.GateDesc) == 24
+
+
+@pytest.mark.parametrize("shape,given", [((0, 64), 0), ((0, 64), 1), ((0, 1), 3), ((1, 64), 0),
+                                         ((64,), 0), ((1, 1), 8)])
+def test_gate_of_an_empty_batch(rec, shape, given):
+    """A gate row per token is an empty gate where there are no tokens."""
+    c, n = lq.norm_residual(torch.zeros(0, 64), torch.zeros(0, 64), gate=torch.zeros(shape),
+                            gate_tokens=given)
+    assert c.shape == n.shape == (0, 64) and descriptor(rec.calls[-1], lq.GateDesc).tokens >= 1
+    with pytest.raises(ValueError, match="does not give"):
+        lq.norm_residual(torch.zeros(0, 64), gate=torch.zeros(2, 64), gate_tokens=given)
