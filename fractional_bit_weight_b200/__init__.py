@@ -526,6 +526,24 @@ def _norm_arg(norm, K, device):
     return norm._arg(K, device)
 
 
+def _apart(a, b, rows):
+    """Whether `rows` rows at a and b, each (address, step, width) in bytes, share no byte. Rows of
+    different steps count as sharing where their whole extents do."""
+    first, last = sorted((a, b))
+    if first[0] + (rows - 1) * first[1] + first[2] <= last[0]:
+        return True
+    shift = (last[0] - first[0]) % first[1]
+    return first[1] == last[1] and first[2] <= shift and shift + last[2] <= first[1]
+
+
+def _check_overlap(out, residual, h, rows):
+    """residual_out may be the residual or h itself; each row is read before it is written. Anywhere
+    else in their memory it would overwrite rows that are still to be read."""
+    for other, name in ((residual, "residual"), (h, "h")):
+        if other is not None and rows and other != out and not _apart(out, other, rows):
+            raise ValueError(f"residual_out overlaps {name}")
+
+
 def _boundary(h, residual, post, pre, gate, gate_tokens, branch_scale, residual_scale,
               residual_out, dtype, codes, whiten):
     """The arguments' checks, outputs and call of lq_norm_residual on the current stream."""
@@ -550,6 +568,12 @@ def _boundary(h, residual, post, pre, gate, gate_tokens, branch_scale, residual_
         r_out = residual_out
         p_out = _arg(r_out, "residual_out", _DTYPES, device, shape)
         rdt = _DTYPES[r_out.dtype]
+    if residual_out is not None:
+        size = r_out.element_size()
+        ldo = ldr if r_out is residual else K
+        _check_overlap((p_out, ldo * size, K * size),
+                       None if residual is None else (pr, ldr * size, K * size),
+                       (ph, ldh * h.element_size(), K * h.element_size()), rows)
     g = None
     if gate is not None:
         pg = _arg(gate, "gate", _DTYPES, device)
@@ -596,7 +620,8 @@ def norm_residual(h, residual=None, post=None, pre=None, gate=None, gate_tokens=
     [ceil(rows / gate_tokens)][K or 1], a row per gate_tokens tokens (0: one row for all, or one
     per token if there are that many). Returns (c in residual's type, n in `dtype`, h's if None).
     residual_out=residual updates it in place; without a residual c is only written if
-    residual_out is given (else None is returned for it)."""
+    residual_out is given (else None is returned for it). A residual_out that overlaps h or the
+    residual in any other way is refused."""
     device = _device_of(h, "h")
     if stream is not None or device != _current_device():
         return _over_there(

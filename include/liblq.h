@@ -334,7 +334,8 @@ typedef struct lq_gate_desc {
  *   h      [rows][K] device, row t at element t * ldh (ldh >= K): the block's output.
  *   r      [rows][K] device, row t at element t * ldr (ldr >= K), or NULL.
  *   r_out  [rows][K] of type rdt: c, or NULL. Dense, unless r_out == r: then in place at r's
- *          stride. No other output may overlap an input.
+ *          stride. It may also be h, if h is dense and its type as wide as rdt. No output may
+ *          overlap an input in any other way.
  *   n_out  [rows][K] of type ndt, dense: n, or NULL.
  *   q, q_scale  T(n) as int8 rows and scales exactly as lq_quant_i8 makes them, or both NULL
  *          (T is then not used).

@@ -43,3 +43,15 @@ def test_boundary_of_an_empty_batch():
         assert c.shape == n.shape == (0, 64)
         c, q, s = lq.norm_residual_i8(h, h, None, None, gate, tokens, block=64)
         assert q.shape == (0, 64) and s.shape == (0,)
+
+
+def test_boundary_in_place_over_its_input():
+    """c may take the place of h as it may that of the residual."""
+    g = gen(2)
+    for rows, K in ((3, 1000), (400, 1000), (2, 20000), (5, 333)):
+        pre = lq.Norm("rms", rand((K,), F32, g))
+        h, r = rand((rows, K), BF16, g), rand((rows, K), BF16, g)
+        want = lq.norm_residual(h, r, pre, pre)
+        for args, out in (((h.clone(), r), 0), ((h, r.clone()), 1)):
+            c, n = lq.norm_residual(*args, pre, pre, residual_out=args[out])
+            assert c is args[out] and torch.equal(c, want[0]) and torch.equal(n, want[1])

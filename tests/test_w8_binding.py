@@ -98,3 +98,34 @@ def test_gate_of_an_empty_batch(rec, shape, given):
     assert c.shape == n.shape == (0, 64) and descriptor(rec.calls[-1], lq.GateDesc).tokens >= 1
     with pytest.raises(ValueError, match="does not give"):
         lq.norm_residual(torch.zeros(0, 64), gate=torch.zeros(2, 64), gate_tokens=given)
+
+
+def test_residual_out_over_inputs(rec):
+    """In place or apart; what would overwrite rows before they are read is refused."""
+    rows, K = 6, 64
+    buf = torch.zeros(4 * rows * K)
+    view = lambda at, step=K, n=rows: buf.as_strided((n, K), (step, 1), at)  # noqa: E731
+    h, r = torch.zeros(rows, K), view(0)
+    strided = view(0, 2 * K)
+    for h_, r_, out in ((h, r, r), (h, r, view(0)), (h, strided, strided), (h, r, view(rows * K)),
+                        (h, strided, view(2 * rows * K)), (r, None, view(0)), (r, view(rows * K), r),
+                        (strided, view(K, 2 * K), None), (h, None, view(5))):
+        lq.norm_residual(h_, r_, residual_out=out)
+    inside = view(K, 2 * K)         # every other row of the same memory
+    lq.norm_residual(strided, inside, residual_out=inside)
+    calls = len(rec.calls)
+    for h_, r_, out, name in ((h, r, view(K), "residual"), (h, view(K), view(0), "residual"),
+                              (h, strided, view(0), "residual"), (h, strided, view(K), "residual"),
+                              (view(8), None, view(0), "h"), (strided, None, view(0), "h"),
+                              (h, r, view(1), "residual"),
+                              (r, view(2 * rows * K), view(K), "h")):
+        with pytest.raises(ValueError, match="residual_out overlaps " + name):
+            lq.norm_residual(h_, r_, residual_out=out)
+    with pytest.raises(ValueError, match="residual_out overlaps h"):
+        lq.norm_residual(view(8, 2 * K), strided, residual_out=strided)
+    half = buf.view(torch.bfloat16)[:rows * K].view(rows, K)
+    with pytest.raises(ValueError, match="residual_out overlaps h"):
+        lq.norm_residual(half, None, residual_out=r)
+    assert len(rec.calls) == calls
+    empty = torch.zeros(0, K)
+    lq.norm_residual(empty, empty, residual_out=torch.zeros(0, K))
