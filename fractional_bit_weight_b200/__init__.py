@@ -392,8 +392,10 @@ def _rows(t, name, dtypes, device, shape=None):
     return t.data_ptr(), step if rows > 1 else K
 
 
-_current_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream    # of a device, as an address
+# of a build of torch with CUDA; without it no call gets as far (its tensors are not CUDA tensors),
+# but the host-only queries work
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)    # of a device, as an address
 
 
 def _over_there(call, device, stream, inputs):

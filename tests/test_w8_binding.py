@@ -1,6 +1,9 @@
 """What the binding of the 8-bit and boundary operators passes on, refuses and keeps. No GPU is
 used: host and meta tensors stand in for the device's, and a recorder for the library."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -129,3 +132,20 @@ def test_residual_out_over_inputs(rec):
     assert len(rec.calls) == calls
     empty = torch.zeros(0, K)
     lq.norm_residual(empty, empty, residual_out=torch.zeros(0, K))
+
+
+def test_import_with_a_cpu_build_of_torch():
+    """The host-only queries need no CUDA in torch."""
+    code = ("import torch\n"
+            "for name in [n for n in vars(torch._C) if n.startswith('_cuda')]:\n"
+            "    delattr(torch._C, name)\n"
+            "import fractional_bit_weight_b200 as lq\n"
+            "assert lq.gemm_route(1, 4096, 4096, 10, 24) >= 0\n"
+            "assert lq.gemm_i8_route(1, 4096, 4096) >= 0\n"
+            "try:\n"
+            "    lq.quant_i8(torch.zeros(2, 64))\n"
+            "except TypeError:\n"
+            "    print('refused')\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(lq.__file__)))
+    out = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert out.returncode == 0 and out.stdout.strip() == "refused", out.stderr
