@@ -433,6 +433,9 @@ def _int32(n, name):
 
 def _whiten_arg(sign, chan_scale, block, K, device):
     if not block:
+        if sign is not None or chan_scale is not None:
+            raise ValueError("sign and chan_scale are parts of T, which block = 0 leaves out "
+                             "(block = 1 applies them without mixing)")
         return None
     return ctypes.byref(WhitenDesc(
         None if sign is None else _arg(sign, "sign", _I8, device, (K,)),
@@ -448,7 +451,8 @@ def i8_row_bytes(K):
 def quant_i8(x, sign=None, chan_scale=None, block=0, values=False, stream=None):
     """Symmetric int8 rows of T(x) with a scale per row (see lq_quant_i8).
 
-    x [rows][K] f32/f16/bf16; its rows may lie apart. Returns (q int8 [rows][i8_row_bytes(K)],
+    x [rows][K] f32/f16/bf16; its rows may lie apart. block = 0 leaves T out, 1 applies sign and
+    chan_scale alone. Returns (q int8 [rows][i8_row_bytes(K)],
     scale fp32 [rows]); with values=True also scale * q in x's type, [rows][K]."""
     device = _device_of(x, "x")
     if stream is not None or device != _current_device():

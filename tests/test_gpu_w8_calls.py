@@ -55,3 +55,26 @@ def test_boundary_in_place_over_its_input():
         for args, out in (((h.clone(), r), 0), ((h, r.clone()), 1)):
             c, n = lq.norm_residual(*args, pre, pre, residual_out=args[out])
             assert c is args[out] and torch.equal(c, want[0]) and torch.equal(n, want[1])
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("rows,K", [(3, 264), (300, 2048), (2, 333), (300, 1001), (2, 20000)])
+def test_channel_scales_without_rotation(rows, K, dtype):
+    """block = 1: the codes of sign . chan_scale . x. The scales are powers of two, so that the
+    products are exact and the codes those of the definition."""
+    g = gen(K)
+    x = rand((rows, K), dtype, g)
+    scale = torch.exp2(torch.randint(-3, 4, (K,), generator=g, device=DEV).float())
+    sign = torch.randint(0, 2, (K,), generator=g, device=DEV).to(torch.int8) * 2 - 1
+    for sg, cs in ((sign, None), (None, scale), (sign, scale)):
+        q, s, v = lq.quant_i8(x, sign=sg, chan_scale=cs, block=1, values=True)
+        t = x.double() * (1 if sg is None else sg.double()) * (1 if cs is None else cs.double())
+        want, ws = ref.codes(t)
+        off = 127 * (q[:, :K].double() / 127 - t / t.abs().amax(1, keepdim=True))
+        # half to even from an approximate quotient: a code next to a border may fall either way
+        assert (off.abs() <= 0.5 + 127 * 2 * ref.EPS32).all() and not q[:, K:].any()
+        assert ((s.double() - ws).abs() <= 2 * ref.EPS32 * ws).all()
+        assert torch.equal(v, (q[:, :K].float() * s[:, None]).to(dtype))
+        _, q2, s2, n = lq.norm_residual_i8(x, sign=sg, chan_scale=cs, block=1, dtype=F32)
+        assert torch.equal(n, x.float()) and torch.equal(s, s2)
+        assert int((q != q2).sum()) <= int((off.abs() > 0.5 - 127 * 2 * ref.EPS32).sum())

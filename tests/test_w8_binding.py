@@ -149,3 +149,20 @@ def test_import_with_a_cpu_build_of_torch():
     root = os.path.dirname(os.path.dirname(os.path.abspath(lq.__file__)))
     out = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
     assert out.returncode == 0 and out.stdout.strip() == "refused", out.stderr
+
+
+def test_parts_of_t_without_t(rec):
+    """sign and chan_scale belong to T: with block = 0 they would be dropped without a word."""
+    x, sign, scale = torch.zeros(4, 64), torch.ones(64, dtype=torch.int8), torch.ones(64)
+    for parts in (dict(sign=sign), dict(chan_scale=scale), dict(sign=sign, chan_scale=scale)):
+        for call in (lambda **kw: lq.quant_i8(x, **kw), lambda **kw: lq.norm_residual_i8(x, **kw)):
+            with pytest.raises(ValueError, match="block = 0"):
+                call(**parts)
+            assert not rec.calls
+            call(**parts, block=1)
+            d = descriptor(rec.calls.pop(), lq.WhitenDesc)
+            assert d.block == 1
+            assert d.sign == (sign.data_ptr() if "sign" in parts else None)
+            assert d.chan_scale == (scale.data_ptr() if "chan_scale" in parts else None)
+    lq.quant_i8(x)
+    lq.norm_residual_i8(x)
