@@ -17,7 +17,8 @@ __all__ = [
     "new_workspace",
     "device_status", "check_wait_timeout", "NOALLOC_SCRATCH_BYTES",
     "i8_row_bytes", "quant_i8", "Norm", "norm_residual", "norm_residual_i8", "gemm_i8",
-    "gemm_i8_route", "gemm_i8_plan", "new_i8_workspace", "GEMM_I8_WORKSPACE_BYTES",
+    "gemm_i8_route", "gemm_i8_plan", "new_i8_workspace",
+    "default_i8_workspace", "GEMM_I8_WORKSPACE_BYTES",
 ]
 
 NOALLOC_SCRATCH_BYTES = 8 << 20   # LQ_NOALLOC_SCRATCH_BYTES
@@ -685,13 +686,35 @@ def new_i8_workspace(device="cuda"):
     return torch.zeros(GEMM_I8_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
 
 
+_I8_WORKSPACES = {}     # by device index, for the calls that are given none
+
+
+def default_i8_workspace(device="cuda"):
+    """The workspace of a device's gemm_i8 calls that are given none: device_status reads there
+    whether one of them failed on the device. Made by the first such call that is not captured (or
+    here); a call captured before that gets one of its own, whose status is lost."""
+    device = torch.device(device)
+    index = torch.cuda.current_device() if device.index is None else device.index
+    workspace = _I8_WORKSPACES.get(index)
+    return _new_default(index, device) if workspace is None else workspace
+
+
+def _new_default(index, device):
+    workspace = new_i8_workspace(device)
+    if torch.cuda.is_current_stream_capturing():
+        return workspace        # the graph's own memory
+    torch.cuda.current_stream(device).synchronize()     # zero before another stream's call
+    return _I8_WORKSPACES.setdefault(index, workspace)
+
+
 def gemm_i8(xq, xs, wq, ws, K=None, bias=None, dtype=torch.float32, y=None, workspace=None,
             stream=None, route=None):
     """y[t][n] = (xq[t] . wq[n]) * (xs[t] * ws[n]) + bias[n], [batch][N] of `dtype`.
 
     xq [batch][i8_row_bytes(K)] and wq [N][i8_row_bytes(K)] int8, xs [batch], ws [N] and bias [N]
     fp32. K None: the whole stored rows (quant_i8 pads them with zeros). route=None lets the
-    library pick the kernel; an I8_ROUTE_* code runs that one."""
+    library pick the kernel; an I8_ROUTE_* code runs that one. workspace None: the device's
+    default_i8_workspace()."""
     device = _device_of(xq, "xq")
     if stream is not None or device != _current_device():
         return _over_there(lambda: gemm_i8(xq, xs, wq, ws, K, bias, dtype, y, workspace, None,
@@ -718,7 +741,9 @@ def gemm_i8(xq, xs, wq, ws, K=None, bias=None, dtype=torch.float32, y=None, work
     else:
         _arg(y, "y", _DTYPES, device, (batch, N))
     if workspace is None:
-        workspace = new_i8_workspace(xq.device)
+        workspace = _I8_WORKSPACES.get(device)
+        if workspace is None:
+            workspace = _new_default(device, xq.device)
     pw = _arg(workspace, "workspace", (torch.uint8,), device)
     _check(lib().lq_gemm_i8(pxq, pxs, batch, pwq, pws, pb, K, N, y.data_ptr(), _DTYPES[y.dtype],
                             pw, workspace.numel(), -1 if route is None else _int32(route, "route"),

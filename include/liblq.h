@@ -381,7 +381,8 @@ LQ_API lq_status lq_gemm_i8_plan(int32_t batch, int32_t K, int32_t N, int32_t ro
  *   xs [batch], ws [N] fp32 device; bias [N] fp32 device or NULL.
  *   y  [batch][N] of type ydt, dense.
  *   workspace: LQ_GEMM_I8_WORKSPACE_BYTES bytes, 256-byte aligned, zero-filled once before its
- *   first use; holds the status word that lq_device_status reads.
+ *   first use; holds the status word that lq_device_status reads. Nothing else is kept there, so
+ *   calls on different streams may share it.
  *   route: -1 lets the library choose, an LQ_I8_ROUTE_* code asks for that kernel.
  * Errors: LQ_EINVAL (null or misaligned pointers, batch < 0, N < 0, K < 1, unknown dtype or
  * route, workspace too small), LQ_EUNSUPPORTED (K > LQ_MAX_I8_K, batch or N > 2^30, a route that

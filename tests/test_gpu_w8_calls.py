@@ -78,3 +78,42 @@ def test_channel_scales_without_rotation(rows, K, dtype):
         _, q2, s2, n = lq.norm_residual_i8(x, sign=sg, chan_scale=cs, block=1, dtype=F32)
         assert torch.equal(n, x.float()) and torch.equal(s, s2)
         assert int((q != q2).sum()) <= int((off.abs() > 0.5 - 127 * 2 * ref.EPS32).sum())
+
+
+def test_status_of_calls_without_a_workspace():
+    g = gen(3)
+    q, s = lq.quant_i8(rand((40, 256), BF16, g))
+    wq, sw = lq.quant_i8(rand((100, 256), BF16, g))
+    y = lq.gemm_i8(q, s, wq, sw)
+    ws = lq.default_i8_workspace()
+    assert lq.device_status(ws) == (lq.LQ_OK, 0)
+    # a bounded wait that runs out records itself there; the next product is right
+    lq.check_wait_timeout(ws, 5)
+    assert lq.device_status(ws) == (lq.LQ_ETIMEOUT, lq.LQ_ETIMEOUT)
+    assert torch.equal(y, lq.gemm_i8(q, s, wq, sw)) and lq.device_status(ws) == (lq.LQ_OK, 0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    y2 = lq.gemm_i8(q, s, wq, sw, stream=side)
+    side.synchronize()
+    assert torch.equal(y, y2) and lq.default_i8_workspace("cuda:0") is ws
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = lq.gemm_i8(q, s, wq, sw)
+    out.zero_()
+    graph.replay()
+    assert torch.equal(out, y) and lq.default_i8_workspace() is ws
+
+
+def test_first_call_captured(monkeypatch):
+    """A call captured before any other makes its workspace part of the graph."""
+    monkeypatch.setattr(lq, "_I8_WORKSPACES", {})
+    g = gen(4)
+    q, s = lq.quant_i8(rand((40, 256), BF16, g))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = lq.gemm_i8(q, s, q, s)
+    assert not lq._I8_WORKSPACES
+    graph.replay()
+    assert torch.equal(out, lq.gemm_i8(q, s, q, s))

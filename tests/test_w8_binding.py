@@ -166,3 +166,29 @@ def test_parts_of_t_without_t(rec):
             assert d.chan_scale == (scale.data_ptr() if "chan_scale" in parts else None)
     lq.quant_i8(x)
     lq.norm_residual_i8(x)
+
+
+def test_calls_without_a_workspace_share_one(rec, monkeypatch):
+    """The status word of a call that is given no workspace is where default_i8_workspace() says."""
+    capturing = [True]
+    stream = type("Stream", (), {"synchronize": lambda self: None})()
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing[0])
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: stream)
+    monkeypatch.setattr(lq, "_I8_WORKSPACES", {}, raising=False)
+    q, s = torch.zeros(4, 64, dtype=torch.int8), torch.ones(4)
+
+    def workspace_of(**kw):
+        lq.gemm_i8(q, s, q, s, **kw)
+        return rec.calls[-1][1][10]
+
+    workspace_of()
+    assert not lq._I8_WORKSPACES    # a captured call's workspace belongs to its graph
+    capturing[0] = False
+    at = workspace_of()
+    assert at == workspace_of() == lq._I8_WORKSPACES[HOST].data_ptr()
+    capturing[0] = True
+    assert at == workspace_of()
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: HOST)
+    assert at == lq.default_i8_workspace().data_ptr()
+    own = torch.zeros(256, dtype=torch.uint8)
+    assert workspace_of(workspace=own) == own.data_ptr()
