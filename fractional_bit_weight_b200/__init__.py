@@ -665,7 +665,8 @@ def _sizes(batch, K, N):
 
 
 def gemm_i8_route(batch, K, N):
-    """Which kernel lq_gemm_i8 runs for this shape (host-only query; I8_ROUTE_* codes)."""
+    """Which kernel lq_gemm_i8 runs for this shape on the current device, without one on a B200
+    with 148 SMs (launches nothing; I8_ROUTE_* codes)."""
     return int(lib().lq_gemm_i8_route(*_sizes(batch, K, N)))
 
 
@@ -673,7 +674,7 @@ I8_PLAN_FIELDS = ("route", "cluster", "tiles", "rows", "tokens", "chunks", "stag
 
 
 def gemm_i8_plan(batch, K, N, route=None):
-    """The tiles of lq_gemm_i8's tensor-core routes for a shape (host-only query), as a dict."""
+    """The tiles of lq_gemm_i8's tensor-core routes for a shape (launches nothing), as a dict."""
     out = (ctypes.c_int64 * len(I8_PLAN_FIELDS))()
     _check(lib().lq_gemm_i8_plan(*_sizes(batch, K, N),
                                  -1 if route is None else _int32(route, "route"), out),

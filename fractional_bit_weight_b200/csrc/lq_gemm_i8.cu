@@ -30,6 +30,7 @@
 
 #include <cstdarg>
 #include <cstdio>
+#include <mutex>
 
 #include "lq_device.cuh"
 #include "lq_sm100.cuh"
@@ -55,6 +56,30 @@ __device__ __forceinline__ void store_y(const Args& a, int64_t i, float v) {
   if (a.ydt == LQ_BF16) static_cast<__nv_bfloat16*>(a.y)[i] = __float2bfloat16_rn(v);
   else if (a.ydt == LQ_F16) static_cast<__half*>(a.y)[i] = __float2half_rn(v);
   else static_cast<float*>(a.y)[i] = v;
+}
+
+constexpr int kMaxSplit = 8;   // CTAs of a cluster along K
+
+// What the plans go by: the SMs of the current device and how many clusters of 2, 4 and 8 CTAs are
+// resident on them at once (that depends on how the SMs are grouped). Looked up once per device;
+// without a device, a B200 with 148 SMs.
+struct Machine {
+  int sms = 148;
+  int clusters[kMaxSplit + 1] = {0, 148, 74, 0, 33, 0, 0, 0, 15};
+};
+
+void look_up(int dev, Machine* m);
+const Machine& machine() {
+  static Machine of[64];
+  static std::once_flag seen[64];
+  static const Machine none;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    cudaGetLastError();   // not the error of a later call
+    return none;
+  }
+  std::call_once(seen[dev], look_up, dev, &of[dev]);
+  return of[dev];
 }
 
 // ------------------------------------------------------------------ few tokens
@@ -186,8 +211,9 @@ cudaError_t launch_gemv(const Args& a, cudaStream_t st) {
   // Up to 31 warps per SM, which registers let be resident at once, but four to a CTA at least, and
   // some steps for each. One token x 8192 x 10240: 18.0 us with four warps (17 per SM), 19.2 with
   // eight (35); 8192 x 28672: 41.0 with four (48), 42.4 with two (24).
+  const int most = 31 * machine().sms;
   int warps = 16;
-  while ((warps > 4 && (int64_t)ctas * warps > 148 * 31) || (warps > 1 && (warps / 2) * 64 * U >= a.K))
+  while ((warps > 4 && (int64_t)ctas * warps > most) || (warps > 1 && (warps / 2) * 64 * U >= a.K))
     warps /= 2;
   const size_t smem = (size_t)warps * MT * NT * 128 * sizeof(int);
   static int smem_set[64];
@@ -660,10 +686,7 @@ constexpr size_t kMaxSmem = 227 * 1024;
 // the reverse, and tcgen05.alloc waits without a limit. So every cluster asks for this much. A CTA
 // without a cluster waits for no other with its tensor memory held, so it may share an SM with any.
 constexpr size_t kAloneSmem = kMaxSmem / 2 + 1024;
-constexpr int kMaxSplit = 8;                // CTAs of a cluster along K
 constexpr int kSplitTokens = 128;           // tokens of a kSplit tile: its partials fit the ring
-constexpr int kSplitFit[] = {0, 148, 74, 0, 33, 0, 0, 0, 15};   // clusters of 2, 4 and 8 CTAs that
-                                            // are resident at once on 148 SMs, see make_plan
 constexpr int32_t kMost = 1 << 30;          // tokens, rows: tile coordinates stay in 32 bits
 
 // The tile of a call. Rows of a tile are chosen so that its tiles fill whole waves of the SMs: few
@@ -680,7 +703,9 @@ constexpr int32_t kMost = 1 << 30;          // tokens, rows: tile coordinates st
 // for the first (15 of them 8.2 us, 16 14.6), as the 34th of 4 does (33 10.9, 34 19.1). Split
 // against whole: 32 x 8192 x 1024 5.9 against 9.6 us, 20 x 28672 x 1024 9.2 against 26.1, 64 x 14336
 // x 4096 14.9 against 18.5; and 24 x 1024 x 1024 4.3 against 3.5, 64 x 8192 x 8192 16.5 against 15.8.
-Plan make_plan(int batch, int K, int N, int sms, int force = -1) {
+Plan make_plan(int batch, int K, int N, int force = -1) {
+  const Machine& m = machine();
+  const int sms = m.sms;
   Plan best{};
   double best_cost = 0;
   const int chunks_k = (K + BK - 1) / BK;
@@ -728,7 +753,7 @@ Plan make_plan(int batch, int K, int N, int sms, int force = -1) {
   }
   // clusters along K: the fewest tokens with which all of them are resident at once
   for (int split = 2; split <= kMaxSplit && (force < 0 || force == kSplit); split *= 2) {
-    const int64_t full = (N + kMmaM - 1) / kMmaM, fit = std::max(1, kSplitFit[split] * sms / 148);
+    const int64_t full = (N + kMmaM - 1) / kMmaM, fit = std::max(1, m.clusters[split]);
     const int64_t most = std::max<int64_t>(1, fit / full);       // token tiles
     const int tokens = (int)std::min<int64_t>(kSplitTokens, ((batch + most - 1) / most + 15) / 16 * 16);
     const int tt = (batch + tokens - 1) / tokens;
@@ -780,15 +805,43 @@ bool encode_rows(CUtensorMap* m, const int8_t* p, int64_t K, int64_t rows, int64
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-cudaError_t launch_tc(const Args& a, int force, cudaStream_t st) {
-  const int sms = tc_sm_count();
-  if (sms <= 0) return cudaErrorInvalidDevice;
-  if ((int64_t)((a.N + 127) / 128) * ((a.batch + 15) / 16) > (1 << 30)) return cudaErrorInvalidValue;
-  const Plan p = make_plan(a.batch, a.K, a.N, sms, force);
+const void* const kKernels[3] = {(const void*)gemm_w8_kernel<kOne>,
+                                 (const void*)gemm_w8_kernel<kPair>,
+                                 (const void*)gemm_w8_kernel<kSplit>};
+
+// The tile kernels' limits of shared memory: one size, whatever the plan.
+cudaError_t allow_smem(int kind) {
   static int smem_set[3][64];
-  const void* kernels[3] = {(const void*)gemm_w8_kernel<kOne>, (const void*)gemm_w8_kernel<kPair>,
-                            (const void*)gemm_w8_kernel<kSplit>};
-  cudaError_t e = ensure_smem(kernels[p.kind], p.smem, smem_set[p.kind]);
+  return ensure_smem(kKernels[kind], kMaxSmem, smem_set[kind]);
+}
+
+void look_up(int dev, Machine* m) {
+  int n = 0;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && n > 0)
+    m->sms = n;
+  if (allow_smem(kSplit) == cudaSuccess) {
+    for (int split = 2; split <= kMaxSplit; split *= 2) {
+      cudaLaunchConfig_t cfg{};
+      cfg.gridDim = dim3(split * m->sms);
+      cfg.blockDim = dim3(kThreads);
+      cfg.dynamicSmemBytes = kMaxSmem;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = split;
+      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&n, kKernels[kSplit], &cfg) == cudaSuccess && n > 0)
+        m->clusters[split] = n;
+    }
+  }
+  cudaGetLastError();
+}
+
+cudaError_t launch_tc(const Args& a, int force, cudaStream_t st) {
+  if ((int64_t)((a.N + 127) / 128) * ((a.batch + 15) / 16) > (1 << 30)) return cudaErrorInvalidValue;
+  const Plan p = make_plan(a.batch, a.K, a.N, force);
+  const cudaError_t e = allow_smem(p.kind);
   if (e != cudaSuccess) return e;
   const int shared = p.kind == kPair ? 2 : 1;              // CTAs that share a tile's tokens
   const int group = p.kind == kPair ? 2 : p.split;         // CTAs of a cluster
@@ -799,7 +852,7 @@ cudaError_t launch_tc(const Args& a, int force, cudaStream_t st) {
     return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg{};
   // persistent, except that a cluster along K takes one tile
-  cfg.gridDim = dim3(group * (p.kind == kSplit ? p.tiles : std::min(p.tiles, sms / group)));
+  cfg.gridDim = dim3(group * (p.kind == kSplit ? p.tiles : std::min(p.tiles, machine().sms / group)));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = p.smem;
   cfg.stream = st;
@@ -828,7 +881,7 @@ cudaError_t launch_tc(const Args& a, int force, cudaStream_t st) {
 // 71.8 on 8192 x 57344; not with rows of 4096 (20.0 against 20.4 us on 28672 of them).
 bool few_tokens(int32_t batch, int32_t K, int32_t N) {
   const int64_t weights = (int64_t)N * K;
-  if (batch > LQ_I8_GEMV_MAX_BATCH || (N <= 16 * 74 && K > 14336)) return false;
+  if (batch > LQ_I8_GEMV_MAX_BATCH || (N <= 16 * (machine().sms / 2) && K > 14336)) return false;
   if (N > 16384 && K >= 8192 && weights > 200 * 1000 * 1000) return false;
   return batch <= 8 || weights <= 54 * 1000 * 1000;
 }
@@ -863,7 +916,7 @@ int32_t lq_gemm_i8_route(int32_t batch, int32_t K, int32_t N) {
   using namespace lq::w8;
   if (batch < 1 || N < 1 || K < 1 || K > LQ_MAX_I8_K || batch > kMost || N > kMost) return -1;
   if (few_tokens(batch, K, N)) return LQ_I8_ROUTE_GEMV;
-  return LQ_I8_ROUTE_TC + make_plan(batch, K, N, 148).kind;
+  return LQ_I8_ROUTE_TC + make_plan(batch, K, N).kind;
 }
 
 lq_status lq_gemm_i8_plan(int32_t batch, int32_t K, int32_t N, int32_t route, int64_t* out) {
@@ -874,7 +927,7 @@ lq_status lq_gemm_i8_plan(int32_t batch, int32_t K, int32_t N, int32_t route, in
     return reject(LQ_EINVAL, "lq_gemm_i8_plan: invalid sizes batch=%d K=%d N=%d", batch, K, N);
   if (route != -1 && (route < LQ_I8_ROUTE_TC || route > LQ_I8_ROUTE_SPLIT))
     return reject(LQ_EINVAL, "lq_gemm_i8_plan: route %d has no tiles", route);
-  const Plan p = make_plan(batch, K, N, 148, route < 0 ? -1 : route - LQ_I8_ROUTE_TC);
+  const Plan p = make_plan(batch, K, N, route < 0 ? -1 : route - LQ_I8_ROUTE_TC);
   const int64_t v[LQ_I8_PLAN_FIELDS] = {LQ_I8_ROUTE_TC + p.kind, p.kind == kPair ? 2 : p.split,
                                         (int64_t)p.tiles_n * p.tiles_t, p.rows, p.tokens, p.chunks,
                                         p.stages, (int64_t)p.smem};

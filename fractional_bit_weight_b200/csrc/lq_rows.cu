@@ -944,6 +944,8 @@ bool vectors_ok(const RowArgs& a) {
 
 cudaError_t launch_rows(RowArgs a, int rows, cudaStream_t st) {
   const int block = a.q ? a.T.block : 0;
+  const int sms = tc_sm_count();
+  if (sms <= 0) return cudaErrorInvalidDevice;
   // the wide form while about all its threads are resident at once, and for rows too short to give
   // a thread of the small form four vectors
   Shape s = shape_of(a.K, block, 1);
@@ -952,9 +954,9 @@ cudaError_t launch_rows(RowArgs a, int rows, cudaStream_t st) {
   // which HBM bounds as it is (8192 x 8192: 100 us, with prefetches 107).
   a.ahead = a.plain && block == 0 && a.hdt == LQ_F32
                 ? rows
-                : std::max(1, 148 * (a.r ? 3 : 4) * 256 / 2 / std::max(1, (a.K + 31) / 32));
+                : std::max(1, sms * (a.r ? 3 : 4) * 256 / 2 / std::max(1, (a.K + 31) / 32));
   // (160 rows of 8192 with two norms: 7.7 us in the wide form, 5.2 in the other)
-  a.few = (int64_t)rows * s.ctas * s.threads <= 148 * 1024;
+  a.few = (int64_t)rows * s.ctas * s.threads <= sms * 1024;
   if (!a.few && a.K >= 1024) s = shape_of(a.K, block, 4);
   if (!vectors_ok(a)) {
     if (block)

@@ -360,13 +360,14 @@ LQ_API lq_status lq_norm_residual(const void* h, lq_dtype hdt, int64_t ldh, cons
 /* Bytes of the lq_gemm_i8 workspace: the status word. */
 #define LQ_GEMM_I8_WORKSPACE_BYTES 256
 
-/* Which kernel lq_gemm_i8 runs for this shape (LQ_I8_ROUTE_*; host-only query). Returns -1 on
- * invalid sizes. */
+/* Which kernel lq_gemm_i8 runs for this shape on the current device (LQ_I8_ROUTE_*). Launches
+ * nothing; the first call on a device asks it for its SMs and how many clusters they hold. Without
+ * a device: on a B200 with 148 SMs. Returns -1 on invalid sizes. */
 LQ_API int32_t lq_gemm_i8_route(int32_t batch, int32_t K, int32_t N);
 
 /* The tiles of the tensor-core routes for this shape; route: -1 for the plan that the library
- * compares its choice by, or one of LQ_I8_ROUTE_TC to LQ_I8_ROUTE_SPLIT. Host-only, touches no
- * device: it lets tests check the plan's bounds. out[0 .. LQ_I8_PLAN_FIELDS) receives: the route,
+ * compares its choice by, or one of LQ_I8_ROUTE_TC to LQ_I8_ROUTE_SPLIT. Launches nothing and goes
+ * by the device as lq_gemm_i8_route does: it lets tests check the plan's bounds. out[0 .. LQ_I8_PLAN_FIELDS) receives: the route,
  * CTAs per cluster (1: none), tiles, weight rows per CTA and tokens of a tile, 128-byte chunks per
  * stage, ring stages, dynamic shared memory (bytes).
  * Errors: LQ_EINVAL on invalid sizes, a route without tiles or a null out. */
