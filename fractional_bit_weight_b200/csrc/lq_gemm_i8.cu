@@ -875,14 +875,17 @@ cudaError_t launch_tc(const Args& a, int force, cudaStream_t st) {
 // 14336 x 4096, 15.0 against 14.3 on 8192 x 8192 and 43.3 against 38.7 us on 28672 x 8192. With a
 // CTA per 16 rows it leaves half the SMs idle on a layer of up to 1184 rows, where clusters along K
 // win on long ones: at one token 3.8 against 5.1 us on 8192 x 1024, 6.1 against 6.1 us on 14336 x
-// 1024, 12.5 against 8.6 us on 28672 x 1024. On layers that give it more CTAs than are resident at
-// once, the persistent tiles lose nothing between them: at one token 36.4 against 38.4 us on 28672 x
-// 8192 and 23.0 against 23.6 on 8192 x 16384, but 41.7 against 38.6 on 8192 x 28672 and 78.2 against
-// 71.8 on 8192 x 57344; not with rows of 4096 (20.0 against 20.4 us on 28672 of them).
+// 1024, 12.5 against 8.6 us on 28672 x 1024. Eight of its CTAs are resident per SM. On layers that give
+// it more, the second wave is short of CTAs, and the persistent tiles lose nothing between theirs: at
+// one token 24.7 against 25.6 us on 8192 x 18432 (1152 CTAs), but 33.8 against 28.9 on 8192 x 20480
+// (1280), 37.6 against 33.9 on 8192 x 24576, 40.2 against 39.1 on 8192 x 28672, 40.6 against 34.0 on
+// 10240 x 20480; at eight tokens 25.4 against 26.1 on 8192 x 18432, 33.4 against 29.2 on 8192 x 20480.
+// Not with short rows, whose waves are short: 29.9 against 28.7 us on 6144 x 28672, 33.9 against 34.1
+// on 6144 x 34816, 32.1 against 33.4 on 4096 x 50432.
 bool few_tokens(int32_t batch, int32_t K, int32_t N) {
   const int64_t weights = (int64_t)N * K;
   if (batch > LQ_I8_GEMV_MAX_BATCH || (N <= 16 * (machine().sms / 2) && K > 14336)) return false;
-  if (N > 16384 && K >= 8192 && weights > 200 * 1000 * 1000) return false;
+  if (N > 16 * 8 * machine().sms && K >= 8192) return false;
   return batch <= 8 || weights <= 54 * 1000 * 1000;
 }
 

@@ -62,3 +62,13 @@ def test_plan_refusals():
         with pytest.raises(lq.LQError):
             lq.gemm_i8_plan(*bad)
     assert lq.lib().lq_gemm_i8_plan(1, 64, 64, -1, None) == lq.LQ_EINVAL
+
+
+def test_second_wave_of_the_gemv():
+    """Long rows leave the GEMV where its CTAs of 16 rows are more than 8 on each of the 148 SMs."""
+    edge = 16 * 8 * 148
+    for batch in (1, 4, 8):
+        for K in (8192, 10240, 28672):
+            assert lq.gemm_i8_route(batch, K, edge) == lq.I8_ROUTE_GEMV
+            assert lq.gemm_i8_route(batch, K, edge + 1) != lq.I8_ROUTE_GEMV
+        assert lq.gemm_i8_route(batch, 4096, 2 * edge) == lq.I8_ROUTE_GEMV
