@@ -663,21 +663,34 @@ __device__ __forceinline__ void load_raw(uint4 (&raw)[NV][DT::size / 2], const v
   }
 }
 
-// The scale of the whitened row in v, its codes, and the values they stand for.
-template <class HT, int NV, Mode M>
-__device__ __forceinline__ void write_codes(const RowArgs& a, const Reducer& red, int64_t row,
-                                            int64_t off, int n, float (&v)[NV][8]) {
+constexpr uint32_t kInfinity = 0x7f800000u;
+// T adds up to 4096 entries before its 1/sqrt(block), so a row of large finite ones can overflow on
+// the way. Such a row is moved by 2^-64 first, its scale by 2^64 afterwards; next to its largest
+// entry, what that takes from the small ones is nothing.
+constexpr float kDown = 0x1p-64f, kUp = 0x1p64f;
+
+// The largest magnitude of the row in v as the bits of an fp32: they order like the magnitudes, with
+// infinity and the NaNs on top.
+template <int NV>
+__device__ __forceinline__ uint32_t row_top(const Reducer& red, int which, const float (&v)[NV][8]) {
   float big = 0.f;
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
     for (int i = 0; i < 4; ++i) big = max_abs(big, v[j][2 * i], v[j][2 * i + 1]);
-  // across threads as bits: they order like the magnitudes, with infinity and the NaNs on top
-  const uint32_t top = red.max(4, __float_as_uint(big));
-  const bool finite = top < 0x7f800000u;
+  return red.max(which, __float_as_uint(big));
+}
+
+// The scale of the whitened row in v, its codes, and the values they stand for. top: row_top(v);
+// down: v was moved by kDown.
+template <class HT, int NV, Mode M>
+__device__ __forceinline__ void write_codes(const RowArgs& a, const Reducer& red, int64_t row,
+                                            int64_t off, int n, float (&v)[NV][8], uint32_t top,
+                                            bool down) {
   const float amax = __uint_as_float(top);
-  const float scale =
-      finite ? (a.T.block ? amax * a.T.inv_sqrt : amax) / 127.f : __uint_as_float(0x7fffffffu);
+  const float moved = (a.T.block ? amax * a.T.inv_sqrt : amax) / 127.f;
+  const bool finite = top < kInfinity && !(down && moved * kUp > 0x1.fffffep127f);
+  const float scale = finite ? down ? moved * kUp : moved : __uint_as_float(0x7fffffffu);
   if (threadIdx.x == 0 && red.rank == 0) a.q_scale[row] = scale;
   // 127 v and 127 / a must neither overflow nor lose bits: rows of extreme magnitude are moved
   // by a power of two (exact for every entry that can differ from code 0)
@@ -734,6 +747,21 @@ __device__ __forceinline__ void write_codes(const RowArgs& a, const Reducer& red
   else with_type(a.vdt, write);
 }
 
+// The codes of a row of lq_quant_i8 whose T overflowed, from its inputs moved by kDown. Out of line:
+// few rows ever come here, and the others' registers are not to be shared with it.
+template <class HT, int NV, Mode M>
+__device__ __noinline__ void again_from_below(const RowArgs& a, Reducer red, int row, int off, int n,
+                                              float* ex) {
+  uint4 hr[NV][HT::size / 2];
+  float v[NV][8];
+  load_raw<HT, NV, M>(hr, a.h, (int64_t)row * a.ldh + off, n);
+#pragma unroll
+  for (int j = 0; j < NV; ++j) unpack8<HT>(hr[j][0], hr[j][HT::size / 2 - 1], v[j]);
+  scale_all<NV>(v, kDown);
+  apply_whiten<NV, M>(v, a.T, n, off, ex);
+  write_codes<HT, NV, M>(a, red, row, off, n, v, row_top<NV>(red, 3, v), true);
+}
+
 // n entries of `size` bytes of an input into L2
 __device__ __forceinline__ void prefetch_row(const void* p, int64_t first, int n, int size) {
   const char* src = static_cast<const char*>(p) + first * size;
@@ -771,9 +799,17 @@ __device__ __forceinline__ void work_row(const RowArgs& a, const Reducer& red, i
   if (a.n_out) store_all<NV, M>(v, a.n_out, a.ndt, row * a.K + off, n);
   if (!a.q) return;
 
+  bool down = false;
   if constexpr (M != kStrided)
-    if (a.T.block) apply_whiten<NV, M>(v, a.T, n, off, ex);
-  write_codes<HT, NV, M>(a, red, row, off, n, v);
+    if (a.T.block) {
+      // behind a norm only a weight of 1e30 would make entries that large
+      if (!a.pre.kind && row_top<NV>(red, 3, v) >= __float_as_uint(kUp)) {
+        down = true;
+        scale_all<NV>(v, kDown);
+      }
+      apply_whiten<NV, M>(v, a.T, n, off, ex);
+    }
+  write_codes<HT, NV, M>(a, red, row, off, n, v, row_top<NV>(red, 4, v), down);
 }
 
 // RT: the residual's type, None without one (then r_out, if any, has type a.rdt)
@@ -818,8 +854,16 @@ __global__ void __launch_bounds__(Form<NV, has_r<RT>()>::kThreads, Form<NV, has_
       if constexpr (is_plain<RT>())
         if (a.T.block) apply_whiten<NV, M>(v, a.T, n, off, ex);
     }
-    if constexpr (is_plain<RT>()) write_codes<HT, NV, M>(a, red, row, off, n, v);
-    else work_row<HT, RT, NV, M>(a, red, row, off, n, v, [&](auto add) {
+    if constexpr (is_plain<RT>()) {
+      const uint32_t top = row_top<NV>(red, 4, v);
+      // an infinity or a NaN, or sums of T that overflowed (65504 times 4096 does not)
+      if constexpr (!(std::is_same<RT, PlainMma>::value && HT::dt == LQ_F16))
+        if (a.T.block && top >= kInfinity) {
+          again_from_below<HT, NV, M>(a, red, row, off, n, ex);
+          return;
+        }
+      write_codes<HT, NV, M>(a, red, row, off, n, v, top, false);
+    } else work_row<HT, RT, NV, M>(a, red, row, off, n, v, [&](auto add) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         float w[8];

@@ -291,8 +291,10 @@ LQ_API int64_t lq_i8_row_bytes(int32_t K);
  *     a = max_k |v[k]|,  scale[t] = a / 127,  q[t][k] = round(127 v[k] / a)
  * The quotient is rounded once, half to even (with T, from v as fp32 holds it, to within 127 units
  * of 2^-24); q lies in -127..127. A row of zeros gives scale 0
- * and codes 0. A row that holds an infinity or a NaN gives scale NaN and codes 0, so that it
- * reads NaN behind lq_gemm_i8.
+ * and codes 0. A row that holds an infinity or a NaN, or whose scale passes the largest fp32 (a
+ * chan_scale may do that), gives scale NaN and codes 0, so that it reads NaN behind lq_gemm_i8.
+ * Finite rows up to the largest entries of their type have the codes of T(x), though its sums pass
+ * fp32 on the way.
  *   x       [rows][K] device, row t at element t * ldx (ldx >= K).
  *   T       as for lq_gemm (NULL = identity).
  *   q       [rows][lq_i8_row_bytes(K)] int8 device, 16-byte aligned.
@@ -338,7 +340,8 @@ typedef struct lq_gate_desc {
  *          overlap an input in any other way.
  *   n_out  [rows][K] of type ndt, dense: n, or NULL.
  *   q, q_scale  T(n) as int8 rows and scales exactly as lq_quant_i8 makes them, or both NULL
- *          (T is then not used).
+ *          (T is then not used). With pre and T, entries of n from 2^128 / block on (a weight of
+ *          some 1e30) read as infinities.
  * Errors: LQ_EINVAL (null or misaligned pointers, no output at all, q without q_scale, rows < 0,
  * K < 1, strides < K, unknown dtype or norm kind, bad eps, gate cols or tokens, bad T),
  * LQ_EUNSUPPORTED (K > LQ_MAX_ROW, Hadamard block > LQ_MAX_HADAMARD), LQ_ECUDA. rows = 0 is a

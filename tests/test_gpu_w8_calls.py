@@ -117,3 +117,63 @@ def test_first_call_captured(monkeypatch):
     assert not lq._I8_WORKSPACES
     graph.replay()
     assert torch.equal(out, lq.gemm_i8(q, s, q, s))
+
+
+def check_whitened(x, sign, chan, block, out):
+    """Codes, scales and (or None) values of T(x) against 64 bits, as far as fp32 sums may be off."""
+    q, scale, values = out
+    K = x.shape[1]
+    v, dv = ref.whiten(x, sign, chan, block)
+    a, da = v.abs().amax(1), dv.amax(1)
+    # the maximum's error, then its products with 1/sqrt(block) and 1/127
+    assert ((scale.double() - a / 127).abs() <= (da + 2 * ref.EPS32 * a) / 127).all()
+    off = 127 * (dv + da[:, None]) / (a - da)[:, None] + 1e-12
+    assert ((q[:, :K].double() - 127 * v / a[:, None]).abs() <= 0.5 + off).all()
+    assert not q[:, K:].any()
+    if values is not None:
+        assert torch.equal(values, (q[:, :K].float() * scale[:, None]).to(x.dtype))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("block,K", [(4, 36), (64, 320), (256, 1024), (256, 8192), (1024, 20480),
+                                     (4096, 8192)])
+@pytest.mark.parametrize("rows", [8, 520])
+def test_largest_rows_under_rotation(rows, block, K, dtype):
+    """Finite rows whose sums pass the largest fp32 before T's 1/sqrt(block), beside ordinary ones
+    and ones that hold an infinity or a NaN."""
+    g = gen(block + K)
+    x = rand((rows, K), F32, g)
+    sign = torch.randint(0, 2, (K,), generator=g, device=DEV).to(torch.int8) * 2 - 1
+    top = torch.finfo(dtype).max
+    for i in (0, 1):
+        x[i::8] = (x[i::8] / x[i::8].abs().amax(1, keepdim=True)).double().mul(top).float()
+    x[2::8] = top * sign.float()        # every sum of a block at its largest
+    x[3::8] *= 2.0 ** 100 if dtype != F16 else 1.0
+    x = x.to(dtype)
+    x[4::8, K // 2] = float("inf")
+    x[5::8, K - 1] = float("nan")
+    bad = torch.zeros(rows, dtype=torch.bool, device=DEV)
+    bad[4::8] = bad[5::8] = True
+    scale = torch.rand(K, generator=g, device=DEV) + 0.25
+    for cs in (None, scale):
+        out = lq.quant_i8(x, sign=sign, chan_scale=cs, block=block, values=True)
+        q, s, v = out
+        assert torch.isnan(s[bad]).all() and not q[bad].any() and torch.isnan(v[bad]).all()
+        check_whitened(x[~bad], sign, cs, block, [t[~bad] for t in out])
+        # rows off alignment, and the same rows as a branch without norms
+        pad = torch.zeros(rows, K + 1, dtype=dtype, device=DEV)
+        pad[:, 1:] = x
+        for q2, s2 in (lq.quant_i8(pad[:, 1:], sign=sign, chan_scale=cs, block=block),
+                       lq.norm_residual_i8(x, sign=sign, chan_scale=cs, block=block)[1:]):
+            assert torch.isnan(s2[bad]).all() and not q2[bad].any()
+            check_whitened(x[~bad], sign, cs, block, (q2[~bad], s2[~bad], None))
+
+
+def test_scales_past_fp32_read_as_nan():
+    """A channel scale may take T(x) / 127 past the largest fp32: such a row has no scale."""
+    x = torch.full((2, 256), torch.finfo(F32).max, device=DEV)
+    x[1] = 1.0
+    cs = torch.full((256,), 2.0 ** 20, device=DEV)
+    q, s, v = lq.quant_i8(x, chan_scale=cs, block=256, values=True)
+    assert torch.isnan(s[0]) and not q[0].any() and torch.isnan(v[0]).all()
+    check_whitened(x[1:], None, cs, 256, (q[1:], s[1:], v[1:]))
