@@ -122,92 +122,77 @@ __device__ __forceinline__ uint4 ld_token_end(const int8_t* row, int k, int K) {
   return v;
 }
 
-// One CTA: 16 MT weight rows x 8 NT tokens. Its warps take steps of 64 U inputs in turn, so that
-// the CTA reads a few KB of each row at a time.
-template <int MT, int NT, int U>
+// One CTA: 16 weight rows x 8 NT tokens. Its warps take steps of 64 U inputs in turn, so that the
+// CTA reads a few KB of each row at a time.
+template <int NT, int U>
 __global__ void __launch_bounds__(512) gemv_w8_kernel(const __grid_constant__ Args a) {
-  extern __shared__ int part[];   // [warps][MT][NT][4][32]
+  extern __shared__ int part[];   // [warps][NT][4][32]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int g = lane >> 2, t = lane & 3;
-  const int n0 = blockIdx.x * (16 * MT);
+  const int n0 = blockIdx.x * 16;
   // rows past N and tokens past the batch repeat the last one; their results are not stored
-  const int8_t* w[MT][2];
+  const int8_t* w[2];
   const int8_t* x[NT];
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      w[m][h] = a.wq + (int64_t)min(n0 + 16 * m + 8 * h + g, a.N - 1) * a.ld + 16 * t;
+  for (int h = 0; h < 2; ++h)
+    w[h] = a.wq + (int64_t)min(n0 + 8 * h + g, a.N - 1) * a.ld + 16 * t;
 #pragma unroll
   for (int i = 0; i < NT; ++i) x[i] = a.xq + (int64_t)min(8 * i + g, a.batch - 1) * a.ld + 16 * t;
-  int c[MT][NT][4] = {};
+  int c[NT][4] = {};
   grid_release();
   grid_wait();
   const int stride = warps * (64 * U);
   int k = warp * (64 * U);
   for (; k + 64 * U <= a.K; k += stride) {
-    uint4 u[U][MT][2];
+    uint4 u[U][2];
 #pragma unroll
     for (int s = 0; s < U; ++s)
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) u[s][m][h] = ld_weights(w[m][h] + k + 64 * s);
+      for (int h = 0; h < 2; ++h) u[s][h] = ld_weights(w[h] + k + 64 * s);
 #pragma unroll
     for (int s = 0; s < U; ++s)
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
         const uint4 v = ld_token(x[i] + k + 64 * s);
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          mma_16832(c[m][i], u[s][m][0].x, u[s][m][1].x, u[s][m][0].y, u[s][m][1].y, v.x, v.y);
-          mma_16832(c[m][i], u[s][m][0].z, u[s][m][1].z, u[s][m][0].w, u[s][m][1].w, v.z, v.w);
-        }
+        mma_16832(c[i], u[s][0].x, u[s][1].x, u[s][0].y, u[s][1].y, v.x, v.y);
+        mma_16832(c[i], u[s][0].z, u[s][1].z, u[s][0].w, u[s][1].w, v.z, v.w);
       }
   }
   // the warp that holds the ragged last step
 #pragma unroll 1
   for (const int end = min(k + 64 * U, (int)a.ld); k < end; k += 64) {
     const bool there = k + 16 * t < (int)a.ld;
-    uint4 u[MT][2];
+    uint4 u[2];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        u[m][h] = there ? ld_weights(w[m][h] + k) : make_uint4(0u, 0u, 0u, 0u);
+    for (int h = 0; h < 2; ++h) u[h] = there ? ld_weights(w[h] + k) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       const uint4 v = ld_token_end(x[i] - 16 * t, k + 16 * t, a.K);
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        mma_16832(c[m][i], u[m][0].x, u[m][1].x, u[m][0].y, u[m][1].y, v.x, v.y);
-        mma_16832(c[m][i], u[m][0].z, u[m][1].z, u[m][0].w, u[m][1].w, v.z, v.w);
-      }
+      mma_16832(c[i], u[0].x, u[1].x, u[0].y, u[1].y, v.x, v.y);
+      mma_16832(c[i], u[0].z, u[1].z, u[0].w, u[1].w, v.z, v.w);
     }
   }
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int i = 0; i < NT; ++i)
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) part[(((warp * MT + m) * NT + i) * 4 + e) * 32 + lane] = c[m][i][e];
+    for (int e = 0; e < 4; ++e) part[((warp * NT + i) * 4 + e) * 32 + lane] = c[i][e];
   __syncthreads();
   // c0, c1: row g, tokens 2t, 2t + 1; c2, c3: row g + 8
-  for (int o = threadIdx.x; o < 16 * MT * 8 * NT; o += blockDim.x) {
-    const int r = o % (16 * MT), tok = o / (16 * MT), n = n0 + r;
+  for (int o = threadIdx.x; o < 16 * 8 * NT; o += blockDim.x) {
+    const int r = o % 16, tok = o / 16, n = n0 + r;
     if (n >= a.N || tok >= a.batch) continue;
-    const int slot = (((r >> 4) * NT + (tok >> 3)) * 4 + ((r >> 3) & 1) * 2 + (tok & 1)) * 32 +
-                     (r & 7) * 4 + ((tok & 7) >> 1);
+    const int slot =
+        ((tok >> 3) * 4 + (r >> 3) * 2 + (tok & 1)) * 32 + (r & 7) * 4 + ((tok & 7) >> 1);
     int acc = 0;
-    for (int v = 0; v < warps; ++v) acc += part[v * (MT * NT * 128) + slot];
+    for (int v = 0; v < warps; ++v) acc += part[v * (NT * 128) + slot];
     store_y(a, (int64_t)tok * a.N + n,
             (float)acc * (a.xs[tok] * a.ws[n]) + (a.bias ? a.bias[n] : 0.f));
   }
 }
 
-template <int MT, int NT, int U>
+template <int NT, int U>
 cudaError_t launch_gemv(const Args& a, cudaStream_t st) {
-  const int ctas = (a.N + 16 * MT - 1) / (16 * MT);
+  const int ctas = (a.N + 15) / 16;
   // Up to 31 warps per SM, which registers let be resident at once, but four to a CTA at least, and
   // some steps for each. One token x 8192 x 10240: 18.0 us with four warps (17 per SM), 19.2 with
   // eight (35); 8192 x 28672: 41.0 with four (48), 42.4 with two (24).
@@ -215,9 +200,9 @@ cudaError_t launch_gemv(const Args& a, cudaStream_t st) {
   int warps = 16;
   while ((warps > 4 && (int64_t)ctas * warps > most) || (warps > 1 && (warps / 2) * 64 * U >= a.K))
     warps /= 2;
-  const size_t smem = (size_t)warps * MT * NT * 128 * sizeof(int);
+  const size_t smem = (size_t)warps * NT * 128 * sizeof(int);
   static int smem_set[64];
-  const cudaError_t e = ensure_smem((const void*)gemv_w8_kernel<MT, NT, U>, smem, smem_set);
+  const cudaError_t e = ensure_smem((const void*)gemv_w8_kernel<NT, U>, smem, smem_set);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(ctas);
@@ -229,7 +214,7 @@ cudaError_t launch_gemv(const Args& a, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, gemv_w8_kernel<MT, NT, U>, a);
+  return cudaLaunchKernelEx(&cfg, gemv_w8_kernel<NT, U>, a);
 }
 
 // ------------------------------------------------------------------ tensor-core tiles
@@ -891,8 +876,8 @@ bool few_tokens(int32_t batch, int32_t K, int32_t N) {
 
 cudaError_t launch(const Args& a, int route, cudaStream_t st) {
   if (route < 0 ? few_tokens(a.batch, a.K, a.N) : route == LQ_I8_ROUTE_GEMV) {
-    if (a.batch <= 8) return launch_gemv<1, 1, 2>(a, st);
-    return launch_gemv<1, 2, 4>(a, st);
+    if (a.batch <= 8) return launch_gemv<1, 2>(a, st);
+    return launch_gemv<2, 4>(a, st);
   }
   return launch_tc(a, route < 0 ? -1 : route - LQ_I8_ROUTE_TC, st);   // the kinds in route order
 }
