@@ -28,8 +28,6 @@
 // its own; the shared memory of clusters (kAloneSmem) keeps it from waiting for ever.
 #include <cuda.h>
 
-#include <cstdarg>
-#include <cstdio>
 #include <mutex>
 
 #include "lq_device.cuh"
@@ -882,25 +880,13 @@ cudaError_t launch(const Args& a, int route, cudaStream_t st) {
   return launch_tc(a, route < 0 ? -1 : route - LQ_I8_ROUTE_TC, st);   // the kinds in route order
 }
 
-thread_local char g_err[512];
-
-lq_status reject(lq_status st, const char* fmt, ...) {
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(g_err, sizeof(g_err), fmt, ap);
-  va_end(ap);
-  set_last_error("%s", g_err);
-  return st;
-}
-
-bool al(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-
 }  // namespace w8
 }  // namespace lq
 
 extern "C" {
 
 int32_t lq_gemm_i8_route(int32_t batch, int32_t K, int32_t N) {
+  using namespace lq;
   using namespace lq::w8;
   if (batch < 1 || N < 1 || K < 1 || K > LQ_MAX_I8_K || batch > kMost || N > kMost) return -1;
   if (few_tokens(batch, K, N)) return LQ_I8_ROUTE_GEMV;
@@ -908,6 +894,7 @@ int32_t lq_gemm_i8_route(int32_t batch, int32_t K, int32_t N) {
 }
 
 lq_status lq_gemm_i8_plan(int32_t batch, int32_t K, int32_t N, int32_t route, int64_t* out) {
+  using namespace lq;
   using namespace lq::w8;
   lq::set_last_error("%s", "");
   if (!out) return reject(LQ_EINVAL, "lq_gemm_i8_plan: null out");
@@ -927,6 +914,7 @@ lq_status lq_gemm_i8(const int8_t* xq, const float* xs, int32_t batch, const int
                      const float* ws, const float* bias, int32_t K, int32_t N, void* y,
                      lq_dtype ydt, void* workspace, size_t workspace_bytes, int32_t route,
                      lq_stream stream) {
+  using namespace lq;
   using namespace lq::w8;
   lq::set_last_error("%s", "");
   if (batch < 0) return reject(LQ_EINVAL, "lq_gemm_i8: batch = %d < 0", batch);
@@ -946,10 +934,12 @@ lq_status lq_gemm_i8(const int8_t* xq, const float* xs, int32_t batch, const int
   if (batch == 0 || N == 0) return LQ_OK;
   if (!xq || !xs || !wq || !ws || !y || !workspace)
     return reject(LQ_EINVAL, "lq_gemm_i8: null pointer");
-  if (!al(xq, 16) || !al(wq, 16)) return reject(LQ_EINVAL, "lq_gemm_i8: xq or wq not 16-byte aligned");
-  if (!al(xs, 4) || !al(ws, 4) || !al(bias, 4) || !al(y, ydt == LQ_F32 ? 4 : 2))
+  if (!aligned(xq, 16) || !aligned(wq, 16))
+    return reject(LQ_EINVAL, "lq_gemm_i8: xq or wq not 16-byte aligned");
+  if (!aligned(xs, 4) || !aligned(ws, 4) || !aligned(bias, 4) || !aligned(y, ydt == LQ_F32 ? 4 : 2))
     return reject(LQ_EINVAL, "lq_gemm_i8: misaligned xs, ws, bias or y");
-  if (!al(workspace, 256)) return reject(LQ_EINVAL, "lq_gemm_i8: workspace not 256-byte aligned");
+  if (!aligned(workspace, 256))
+    return reject(LQ_EINVAL, "lq_gemm_i8: workspace not 256-byte aligned");
   if (workspace_bytes < LQ_GEMM_I8_WORKSPACE_BYTES)
     return reject(LQ_EINVAL, "lq_gemm_i8: workspace of %zu bytes, %d needed", workspace_bytes,
                   LQ_GEMM_I8_WORKSPACE_BYTES);

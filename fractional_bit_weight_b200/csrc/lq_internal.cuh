@@ -36,6 +36,13 @@ __device__ __forceinline__ float load_as_f32(const void* p, int dt, int64_t i) {
 
 // Records the reason for a rejected call (read back by lq_last_error on this host thread).
 void set_last_error(const char* fmt, ...);
+// The same, and the status that the call returns.
+template <class... Args>
+lq_status reject(lq_status st, const char* fmt, Args... args) {
+  set_last_error(fmt, args...);
+  return st;
+}
+inline bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 // Validates a whitening descriptor against K (as lq_gemm does) and converts it.
 lq_status whiten_from_desc(const lq_whiten_desc* T, int32_t K, Whiten* out);
 

@@ -17,8 +17,6 @@
 // in blocks of 256 with values 70 (0.64; issue slots 63 % busy), of 4 x 8192 2.9; two norms, gate
 // and residual on 2048 x 8192 30.5 (0.84), on one row of 8192 3.9.
 #include <cmath>
-#include <cstdarg>
-#include <cstdio>
 #include <type_traits>
 
 #include "lq_device.cuh"
@@ -971,19 +969,18 @@ cudaError_t launch_h(const RowArgs& a, int rows, const Shape& s, cudaStream_t st
   return launch_nv<HT, BF16, kVec>(a, rows, s, st);
 }
 
-bool al(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 size_t width(int dt) { return dt == LQ_F32 ? 4 : 2; }
 bool known(int dt) { return dt == LQ_F32 || dt == LQ_F16 || dt == LQ_BF16; }
 
 // 16-byte loads and stores everywhere: K a multiple of 8 and every pointer and stride aligned
 bool vectors_ok(const RowArgs& a) {
-  if (a.K % 8 != 0 || !al(a.h, 16) || a.ldh * width(a.hdt) % 16 != 0) return false;
-  if (a.r && (!al(a.r, 16) || a.ldr * width(a.rdt) % 16 != 0)) return false;
-  if (a.r_out && (!al(a.r_out, 16) || a.ldro * width(a.rdt) % 16 != 0)) return false;
-  if (!al(a.n_out, 16) || !al(a.values, 16) || !al(a.gate, 16)) return false;
+  if (a.K % 8 != 0 || !aligned(a.h, 16) || a.ldh * width(a.hdt) % 16 != 0) return false;
+  if (a.r && (!aligned(a.r, 16) || a.ldr * width(a.rdt) % 16 != 0)) return false;
+  if (a.r_out && (!aligned(a.r_out, 16) || a.ldro * width(a.rdt) % 16 != 0)) return false;
+  if (!aligned(a.n_out, 16) || !aligned(a.values, 16) || !aligned(a.gate, 16)) return false;
   for (const NormArgs* p : {&a.post, &a.pre})
-    if (p->kind && (!al(p->w, 16) || !al(p->b, 16))) return false;
-  return !a.q || !a.T.block || (al(a.T.sign, 8) && al(a.T.chan_scale, 16));
+    if (p->kind && (!aligned(p->w, 16) || !aligned(p->b, 16))) return false;
+  return !a.q || !a.T.block || (aligned(a.T.sign, 8) && aligned(a.T.chan_scale, 16));
 }
 
 cudaError_t launch_rows(RowArgs a, int rows, cudaStream_t st) {
@@ -1014,17 +1011,6 @@ cudaError_t launch_rows(RowArgs a, int rows, cudaStream_t st) {
   return launch_h<BF16>(a, rows, s, st);
 }
 
-thread_local char g_err[512];
-
-lq_status reject(lq_status st, const char* fmt, ...) {
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(g_err, sizeof(g_err), fmt, ap);
-  va_end(ap);
-  set_last_error("%s", g_err);
-  return st;
-}
-
 lq_status check_norm(const lq_norm_desc* d, const char* which, NormArgs* out) {
   out->kind = 0;
   out->eps = 0.f;
@@ -1042,7 +1028,7 @@ lq_status check_norm(const lq_norm_desc* d, const char* which, NormArgs* out) {
   out->w = d->weight;
   out->b = d->bias;
   out->dt = known(d->dtype) ? d->dtype : LQ_F32;
-  if (!al(out->w, width(out->dt)) || !al(out->b, width(out->dt)))
+  if (!aligned(out->w, width(out->dt)) || !aligned(out->b, width(out->dt)))
     return reject(LQ_EINVAL, "%s: misaligned weight or bias", which);
   return LQ_OK;
 }
@@ -1065,6 +1051,7 @@ int64_t lq_i8_row_bytes(int32_t K) { return K < 1 ? -1 : ((int64_t)K + 15) / 16 
 lq_status lq_quant_i8(const void* x, lq_dtype xdt, int32_t rows, int32_t K, int64_t ldx,
                       const lq_whiten_desc* T, int8_t* q, float* scale, void* values,
                       lq_stream stream) {
+  using namespace lq;
   using namespace lq::rows;
   lq::set_last_error("%s", "");
   lq_status st = check_row(rows, K, "lq_quant_i8");
@@ -1073,7 +1060,8 @@ lq_status lq_quant_i8(const void* x, lq_dtype xdt, int32_t rows, int32_t K, int6
   if (rows == 0) return LQ_OK;
   if (!x || !q || !scale) return reject(LQ_EINVAL, "lq_quant_i8: null pointer");
   if (ldx < K) return reject(LQ_EINVAL, "lq_quant_i8: ldx = %lld < K = %d", (long long)ldx, K);
-  if (!al(x, width(xdt)) || !al(q, 16) || !al(scale, 4) || (values && !al(values, width(xdt))))
+  if (!aligned(x, width(xdt)) || !aligned(q, 16) || !aligned(scale, 4) ||
+      (values && !aligned(values, width(xdt))))
     return reject(LQ_EINVAL, "lq_quant_i8: misaligned x, q, scale or values");
   RowArgs a{};
   st = lq::whiten_from_desc(T, K, &a.T);
@@ -1098,6 +1086,7 @@ lq_status lq_norm_residual(const void* h, lq_dtype hdt, int64_t ldh, const void*
                            const lq_gate_desc* gate, float branch_scale, float residual_scale,
                            void* r_out, const lq_norm_desc* pre, void* n_out, lq_dtype ndt,
                            const lq_whiten_desc* T, int8_t* q, float* q_scale, lq_stream stream) {
+  using namespace lq;
   using namespace lq::rows;
   const char* me = "lq_norm_residual";
   lq::set_last_error("%s", "");
@@ -1122,9 +1111,10 @@ lq_status lq_norm_residual(const void* h, lq_dtype hdt, int64_t ldh, const void*
   if (!r_out && !n_out && !q) return reject(LQ_EINVAL, "%s: no output", me);
   if (!h || (gate && !gate->gate)) return reject(LQ_EINVAL, "%s: null pointer", me);
   if (ldh < K || (r && ldr < K)) return reject(LQ_EINVAL, "%s: row stride < K = %d", me, K);
-  if (!al(h, width(hdt)) || ((r || r_out) && (!al(r, width(rdt)) || !al(r_out, width(rdt)))) ||
-      (n_out && !al(n_out, width(ndt))) || !al(q, 16) || !al(q_scale, 4) ||
-      (gate && !al(gate->gate, width(gate->dtype))))
+  if (!aligned(h, width(hdt)) ||
+      ((r || r_out) && (!aligned(r, width(rdt)) || !aligned(r_out, width(rdt)))) ||
+      (n_out && !aligned(n_out, width(ndt))) || !aligned(q, 16) || !aligned(q_scale, 4) ||
+      (gate && !aligned(gate->gate, width(gate->dtype))))
     return reject(LQ_EINVAL, "%s: misaligned pointer", me);
   a.rows = rows;
   a.h = h;
