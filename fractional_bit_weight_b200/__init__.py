@@ -347,6 +347,7 @@ def codebook_round(w, M, d, D, mode=0, b=None, mse=None, workspace=None, stream=
 GEMM_I8_WORKSPACE_BYTES = 256   # LQ_GEMM_I8_WORKSPACE_BYTES
 I8_ROUTE_GEMV, I8_ROUTE_TC, I8_ROUTE_PAIR, I8_ROUTE_SPLIT = 0, 1, 2, 3
 _F32 = (torch.float32,)
+_BYTES = (4, 2, 2)              # of LQ_F32, LQ_F16, LQ_BF16
 _I8 = (torch.int8,)
 _NORM_KINDS = {"rms": 1, "layer": 2}
 
@@ -461,7 +462,8 @@ def quant_i8(x, sign=None, chan_scale=None, block=0, values=False, stream=None):
                            (x, sign, chan_scale))
     px, ldx = _rows(x, "x", _DTYPES, device)
     rows, K = x.shape
-    _int32(rows, "rows"), _int32(K, "K")
+    if rows > _INT32_MAX or K > _INT32_MAX:
+        raise ValueError(f"x of shape {tuple(x.shape)} exceeds 32 bits")
     q = x.new_empty((rows, (K + 15) // 16 * 16), dtype=torch.int8)
     scale = x.new_empty(rows, dtype=torch.float32)
     v = torch.empty_like(x, memory_format=torch.contiguous_format) if values else None
@@ -472,11 +474,6 @@ def quant_i8(x, sign=None, chan_scale=None, block=0, values=False, stream=None):
     return (q, scale, v) if values else (q, scale)
 
 
-def _memory(t):
-    """What a descriptor depends on and what changes when a tensor's `.data` is replaced."""
-    return None if t is None else (t.data_ptr(), t.dtype, t.numel(), t.is_contiguous())
-
-
 class Norm:
     """A norm of lq_norm_residual: kind "rms" or "layer", weight and bias [K] (f32/f16/bf16, of
     one type) or None, eps. Holds its tensors; make it once per layer. Each call takes the tensors
@@ -484,23 +481,22 @@ class Norm:
 
     def __init__(self, kind, weight=None, bias=None, eps=1e-6):
         self.kind, self.weight, self.bias, self.eps = kind, weight, bias, float(eps)
-        self._seen = None
         self._look()
 
+    def __setattr__(self, name, value):
+        super().__setattr__(name, value)
+        if name in ("kind", "weight", "bias", "eps"):
+            super().__setattr__("_held", None)
+
     def _look(self):
-        """Makes the descriptor, after its checks, unless it was made of what is there now."""
-        try:
-            now = (self.kind, self.eps, _memory(self.weight), _memory(self.bias))
-        except AttributeError:      # not a tensor: refused below
-            now = None
-        if now is not None and now == self._seen:
-            return
+        """Makes the descriptor from what the tensors are now, after its checks."""
+        self._held = None
         if self.kind not in _NORM_KINDS:
             raise ValueError(f"unknown norm kind {self.kind!r}, expected one of "
                              f"{sorted(_NORM_KINDS)}")
         device = size = None
         dtype = torch.float32
-        address = {"weight": None, "bias": None}
+        held, address = [], {}
         for t, name in ((self.weight, "weight"), (self.bias, "bias")):
             if t is None:
                 continue
@@ -509,13 +505,22 @@ class Norm:
             address[name] = _arg(t, name, _DTYPES, _device_of(t, name) if device is None else device,
                                  (t.numel(),) if size is None else (size,))
             device, size, dtype = t.get_device(), t.numel(), t.dtype
+            held.append((t, address[name]))
         # a new descriptor: another thread's call may be reading the last one
-        self._ref = ctypes.byref(NormDesc(_NORM_KINDS[self.kind], self.eps, address["weight"],
-                                          address["bias"], _DTYPES[dtype]))
-        self.device, self.size, self._seen = device, size, now
+        self._ref = ctypes.byref(NormDesc(_NORM_KINDS[self.kind], self.eps, address.get("weight"),
+                                          address.get("bias"), _DTYPES[dtype]))
+        self.device, self.size, self._dtype, self._held = device, size, dtype, held
 
     def _arg(self, K, device):
-        self._look()
+        held = self._held
+        if held is None:
+            self._look()
+        else:       # a tensor whose `.data` was replaced is the same tensor over other memory
+            for t, address in held:
+                if (t.data_ptr() != address or t.dtype is not self._dtype or
+                        t.numel() != self.size or not t.is_contiguous()):
+                    self._look()
+                    break
         if self.size is not None and (self.size != K or self.device != device):
             raise ValueError(f"norm over {self.size} entries on cuda:{self.device}, rows of {K} "
                              f"on cuda:{device}")
@@ -533,22 +538,16 @@ def _norm_arg(norm, K, device):
     return norm._arg(K, device)
 
 
-def _apart(a, b, rows):
-    """Whether `rows` rows at a and b, each (address, step, width) in bytes, share no byte. Rows of
-    different steps count as sharing where their whole extents do."""
-    first, last = sorted((a, b))
+def _clash(out, other, rows):
+    """Whether `rows` rows at out overlap those at other, each (address, step, width) in bytes, other
+    than by being the same. Rows of different steps count as overlapping where their extents do."""
+    if out == other:
+        return False
+    first, last = sorted((out, other))
     if first[0] + (rows - 1) * first[1] + first[2] <= last[0]:
-        return True
+        return False
     shift = (last[0] - first[0]) % first[1]
-    return first[1] == last[1] and first[2] <= shift and shift + last[2] <= first[1]
-
-
-def _check_overlap(out, residual, h, rows):
-    """residual_out may be the residual or h itself; each row is read before it is written. Anywhere
-    else in their memory it would overwrite rows that are still to be read."""
-    for other, name in ((residual, "residual"), (h, "h")):
-        if other is not None and rows and other != out and not _apart(out, other, rows):
-            raise ValueError(f"residual_out overlaps {name}")
+    return first[1] != last[1] or first[2] > shift or shift + last[2] > first[1]
 
 
 def _boundary(h, residual, post, pre, gate, gate_tokens, branch_scale, residual_scale,
@@ -557,7 +556,9 @@ def _boundary(h, residual, post, pre, gate, gate_tokens, branch_scale, residual_
     device = h.get_device()
     ph, ldh = _rows(h, "h", _DTYPES, device)
     rows, K = shape = h.shape
-    _int32(rows, "rows"), _int32(K, "K")
+    if rows > _INT32_MAX or K > _INT32_MAX:
+        raise ValueError(f"h of shape {tuple(shape)} exceeds 32 bits")
+    hdt = _DTYPES[h.dtype]
     pr, ldr, rdt = None, 0, 0
     r_out = p_out = None
     if residual is not None:
@@ -575,12 +576,16 @@ def _boundary(h, residual, post, pre, gate, gate_tokens, branch_scale, residual_
         r_out = residual_out
         p_out = _arg(r_out, "residual_out", _DTYPES, device, shape)
         rdt = _DTYPES[r_out.dtype]
-    if residual_out is not None:
-        size = r_out.element_size()
-        ldo = ldr if r_out is residual else K
-        _check_overlap((p_out, ldo * size, K * size),
-                       None if residual is None else (pr, ldr * size, K * size),
-                       (ph, ldh * h.element_size(), K * h.element_size()), rows)
+    if residual_out is not None and rows:
+        # each row of h and the residual is read before its row of residual_out is written, but
+        # other rows may be read later
+        ro, rh = _BYTES[rdt], _BYTES[hdt]
+        out = (p_out, (ldr if r_out is residual else K) * ro, K * ro)
+        if r_out is not residual and residual is not None and \
+                _clash(out, (pr, ldr * ro, K * ro), rows):
+            raise ValueError("residual_out overlaps residual")
+        if _clash(out, (ph, ldh * rh, K * rh), rows):
+            raise ValueError("residual_out overlaps h")
     g = None
     if gate is not None:
         pg = _arg(gate, "gate", _DTYPES, device)
@@ -602,7 +607,7 @@ def _boundary(h, residual, post, pre, gate, gate_tokens, branch_scale, residual_
             raise TypeError(f"dtype {dtype}, expected one of {tuple(_DTYPES)}")
         n = torch.empty_like(h, dtype=dtype, memory_format=torch.contiguous_format)
     _check(lib().lq_norm_residual(
-        ph, _DTYPES[h.dtype], ldh, pr, rdt, ldr, rows, K, _norm_arg(post, K, device), g,
+        ph, hdt, ldh, pr, rdt, ldr, rows, K, _norm_arg(post, K, device), g,
         branch_scale, residual_scale, p_out, _norm_arg(pre, K, device),
         None if n is None else n.data_ptr(), 0 if n is None else _DTYPES[dtype],
         _whiten_arg(*whiten, K, device) if codes else None,
@@ -729,7 +734,8 @@ def gemm_i8(xq, xs, wq, ws, K=None, bias=None, dtype=torch.float32, y=None, work
         K = row
     if (K + 15) // 16 * 16 != row:
         raise ValueError(f"rows of {row} bytes, {(K + 15) // 16 * 16} expected for K = {K}")
-    _sizes(batch, K, N)
+    if batch > _INT32_MAX or K > _INT32_MAX or N > _INT32_MAX:
+        raise ValueError(f"batch = {batch}, K = {K} or N = {N} exceeds 32 bits")
     pxq = _arg(xq, "xq", _I8, device)
     pwq = _arg(wq, "wq", _I8, device, (N, row))
     pxs = _arg(xs, "xs", _F32, device, (batch,))
