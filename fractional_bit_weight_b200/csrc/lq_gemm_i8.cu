@@ -16,10 +16,11 @@
 //    tokens (256 x 256 by a pair of CTAs) with two int32 accumulators in tensor memory, operands
 //    brought by TMA. The weights are the lanes of the accumulator, so the token tile fits the batch
 //    and a warp stores 32 consecutive outputs of a token. Copies and MMAs are issued by an elected
-//    lane each (64 tokens x 8192 x 8192: 30 -> 20 us against a lane chosen by its number).
+//    lane each (64 tokens x 8192 x 8192: 17.1 us, 21.2 with a lane chosen by its number; 128 x 4096 x
+//    4096 8.2 and 10.9).
 //    Measured (device): 2048 tokens 8192 -> 28672 292 us, 3.29 Pop/s, tensor pipe 86 % busy at the
 //    1.56 GHz that the power limit leaves (341 us in a loop of calls); 16 tokens 28672 -> 8192
-//    38.4 us, 6.14 TB/s (0.94 of the copy rate). A layer of few tiles is split along K over the
+//    38.8 us, 6.08 TB/s (0.93 of the copy rate). A layer of few tiles is split along K over the
 //    CTAs of a cluster, which add their sums up through distributed shared memory: 32 tokens 8192
 //    -> 1024 5.9 us (9.6 unsplit), 20 tokens 28672 -> 1024 9.2 us (26.1).
 // Every wait on an mbarrier is bounded in time: on expiry the kernel records LQ_ETIMEOUT in the

@@ -11,11 +11,12 @@
 // runs in one warp's registers and shuffles.
 //
 // What bounds it: HBM for many rows (bytes per entry: h + r + r_out + n or the codes) until the
-// instructions per entry (about 25 for two norms and a gate, 27 for whitened codes with their
+// instructions per entry (about 25 for two norms and a gate, 25 for whitened codes with their
 // values) do; the latency of load -> reductions -> store for a few. Measured (device, us and share
 // of the 6551 GB/s copy rate): codes of 8192 x 8192 fp32 91 (1.01), of 2048 x 28672 bf16 whitened
-// in blocks of 256 with values 70 (0.64; issue slots 63 % busy), of 4 x 8192 2.9; two norms, gate
-// and residual on 2048 x 8192 30.5 (0.84), on one row of 8192 3.9.
+// in blocks of 256 with values 70.4 (0.64; 59 % of the issue slots, a warp's reduction and the
+// shuffles of T in the rest), of 4 x 8192 2.6 and whitened 3.0; two norms, gate and residual on
+// 2048 x 8192 30.8 (0.83), on one row of 8192 3.9.
 #include <cmath>
 #include <type_traits>
 
@@ -320,7 +321,9 @@ __device__ __forceinline__ float max_abs(float a, float b, float c) {
 
 // Reductions over a row: every warp leaves its partial in the shared memory of all the row's CTAs,
 // then all threads read all partials. Each reduction has its own slots, so none waits for the one
-// before to be read.
+// before to be read. An entry of a sum passes through at most 32 additions in its thread (8 with one
+// vector), 5 between lanes, 2 within a read of four partials and one per read: 8 CTAs x 2 reads with
+// four vectors, 8 x 8 with one. So at most 79 roundings of fp32, in either form.
 struct Reducer {
   uint32_t* slots;   // [kReductions][8 CTAs][32 warps]
   int ctas, rank;
@@ -535,8 +538,10 @@ __device__ __forceinline__ void apply_whiten(float (&v)[NV][8], const Whiten& T,
 // T's signs and its butterflies over distance 1, 2, 8 and 16 of 16-bit inputs, as a product: with
 // the eight entries of lane (g, t) as rows g (entries 0 .. 3) and g + 8 (4 .. 7) of a 16 x 16
 // matrix, columns t and the entry's low two bits, each row times the Hadamard matrix of order 16.
-// Its columns are ordered so that every sum lands where its entry came from. The products are
-// exact and summed in fp32.
+// Its columns are ordered so that every sum lands where its entry came from. The products are exact;
+// the tensor core adds the sixteen of a sum in its own way, not as a chain of fp32 additions rounded to
+// nearest. Tests hold all of T to log2(block) + 3 steps of fp32 (2^-23) of the block's sum of
+// magnitudes over sqrt(block).
 template <class HT, int NV, Mode M>
 __device__ __forceinline__ void whiten_mma(float (&v)[NV][8], const uint4 (&raw)[NV][1],
                                            const Whiten& T, int n, int64_t off, float* ex) {
@@ -827,7 +832,8 @@ __global__ void __launch_bounds__(Form<NV, has_r<RT>()>::kThreads, Form<NV, has_
   const int n = min(a.K - off, (8 * NV) * T);
   // all CTAs of the cluster run before one writes to another's shared memory
   if (ctas > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-  // a few rows overlap their start with the kernel before and after (4 x 8192 codes 4.2 -> 3.7 us);
+  // a few rows overlap their start with the kernel before and after (4 x 8192 codes 3.1 -> 2.6 us,
+  // whitened 3.5 -> 3.0, one row through two norms 4.4 -> 3.9);
   // many would give SMs away early (65536 x 256 and two norms 37.4 -> 68.4 us)
   if (NV == 1 && a.few) {
     sm100::grid_release();

@@ -307,7 +307,8 @@ LQ_API lq_status lq_quant_i8(const void* x, lq_dtype xdt, int32_t rows, int32_t 
                              const lq_whiten_desc* T, int8_t* q, float* scale, void* values,
                              lq_stream stream);
 
-/* A norm over the K entries of a row; statistics in fp32.
+/* A norm over the K entries of a row; statistics in fp32, so a row whose squares add up past it (entries
+ * from about 1e19 / sqrt(K) on) is divided by an infinity.
  *   LQ_NORM_RMS:   v / sqrt(mean(v^2) + eps) * weight + bias
  *   LQ_NORM_LAYER: (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps) * weight + bias */
 typedef enum lq_norm_kind { LQ_NORM_RMS = 1, LQ_NORM_LAYER = 2 } lq_norm_kind;
