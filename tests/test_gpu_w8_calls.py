@@ -1,4 +1,8 @@
 """Calls of the 8-bit and boundary operators that the other tests do not make."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -177,3 +181,43 @@ def test_scales_past_fp32_read_as_nan():
     q, s, v = lq.quant_i8(x, chan_scale=cs, block=256, values=True)
     assert torch.isnan(s[0]) and not q[0].any() and torch.isnan(v[0]).all()
     check_whitened(x[1:], None, cs, 256, (q[1:], s[1:], v[1:]))
+
+
+FIRST_CALLS_CAPTURED = """
+import torch
+import fractional_bit_weight_b200 as lq
+x = torch.randn(40, 512, device="cuda")
+w = torch.randn(300, 512, device="cuda")
+wq = torch.zeros(300, 512, dtype=torch.int8, device="cuda")
+ws = torch.zeros(300, device="cuda")
+pre = lq.Norm("rms", torch.ones(512, device="cuda"))
+
+
+def call():
+    q, s = lq.quant_i8(w, block=256)
+    wq.copy_(q)
+    ws.copy_(s)
+    c, q, s = lq.norm_residual_i8(x, x, None, pre, block=256)
+    return [c, q, s] + [lq.gemm_i8(q[:n], s[:n], wq, ws, route=r)
+                        for n, r in ((2, None), (40, None), (40, lq.I8_ROUTE_TC),
+                                     (40, lq.I8_ROUTE_PAIR), (40, lq.I8_ROUTE_SPLIT))]
+
+
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    out = call()
+graph.replay()
+torch.cuda.synchronize()
+for a, b in zip(out, call()):
+    assert torch.equal(a, b)
+print("same")
+"""
+
+
+def test_first_calls_of_a_process_captured():
+    """The library looks the device up and raises its kernels' limits inside a capture."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(lq.__file__)))
+    out = subprocess.run([sys.executable, "-c", FIRST_CALLS_CAPTURED], cwd=root,
+                         capture_output=True, text=True, timeout=300)
+    assert out.returncode == 0 and out.stdout.strip() == "same", out.stderr[-2000:]
