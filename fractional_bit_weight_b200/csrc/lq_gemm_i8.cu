@@ -668,7 +668,8 @@ constexpr size_t kMaxSmem = 227 * 1024;
 // never share one. A CTA of a cluster keeps its tensor memory until its peers have allocated theirs.
 // If CTAs of clusters X and Y shared two SMs, X's could hold one and wait for the other while Y's did
 // the reverse, and tcgen05.alloc waits without a limit. So every cluster asks for this much. A CTA
-// without a cluster waits for no other with its tensor memory held, so it may share an SM with any.
+// without a cluster may share an SM with any: with its tensor memory held it waits only (in grid_wait)
+// for kernels ahead of it on its stream, and those let it start when all their CTAs had theirs.
 constexpr size_t kAloneSmem = kMaxSmem / 2 + 1024;
 constexpr int kSplitTokens = 128;           // tokens of a kSplit tile: its partials fit the ring
 constexpr int32_t kMost = 1 << 30;          // tokens, rows: tile coordinates stay in 32 bits
@@ -801,25 +802,24 @@ cudaError_t allow_smem(int kind) {
 
 void look_up(int dev, Machine* m) {
   int n = 0;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && n > 0)
-    m->sms = n;
-  if (allow_smem(kSplit) == cudaSuccess) {
-    for (int split = 2; split <= kMaxSplit; split *= 2) {
-      cudaLaunchConfig_t cfg{};
-      cfg.gridDim = dim3(split * m->sms);
-      cfg.blockDim = dim3(kThreads);
-      cfg.dynamicSmemBytes = kMaxSmem;
-      cudaLaunchAttribute attr[1];
-      attr[0].id = cudaLaunchAttributeClusterDimension;
-      attr[0].val.clusterDim.x = split;
-      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-      cfg.attrs = attr;
-      cfg.numAttrs = 1;
-      if (cudaOccupancyMaxActiveClusters(&n, kKernels[kSplit], &cfg) == cudaSuccess && n > 0)
-        m->clusters[split] = n;
-    }
+  cudaError_t e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess && n > 0) m->sms = n;
+  if (e == cudaSuccess) e = allow_smem(kSplit);
+  for (int split = 2; split <= kMaxSplit && e == cudaSuccess; split *= 2) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(split * m->sms);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kMaxSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = split;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&n, kKernels[kSplit], &cfg);
+    if (e == cudaSuccess && n > 0) m->clusters[split] = n;
   }
-  cudaGetLastError();
+  if (e != cudaSuccess) cudaGetLastError();   // the launch that follows reports its own
 }
 
 cudaError_t launch_tc(const Args& a, int force, cudaStream_t st) {

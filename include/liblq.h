@@ -307,8 +307,8 @@ LQ_API lq_status lq_quant_i8(const void* x, lq_dtype xdt, int32_t rows, int32_t 
                              const lq_whiten_desc* T, int8_t* q, float* scale, void* values,
                              lq_stream stream);
 
-/* A norm over the K entries of a row; statistics in fp32, so a row whose squares add up past it (entries
- * from about 1e19 / sqrt(K) on) is divided by an infinity.
+/* A norm over the K entries of a row. Its statistics are held in fp32: a row whose squares add up
+ * past that (entries from about 1e19 / sqrt(K) on) is divided by an infinity.
  *   LQ_NORM_RMS:   v / sqrt(mean(v^2) + eps) * weight + bias
  *   LQ_NORM_LAYER: (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps) * weight + bias */
 typedef enum lq_norm_kind { LQ_NORM_RMS = 1, LQ_NORM_LAYER = 2 } lq_norm_kind;
@@ -369,11 +369,12 @@ LQ_API lq_status lq_norm_residual(const void* h, lq_dtype hdt, int64_t ldh, cons
  * a device: on a B200 with 148 SMs. Returns -1 on invalid sizes. */
 LQ_API int32_t lq_gemm_i8_route(int32_t batch, int32_t K, int32_t N);
 
-/* The tiles of the tensor-core routes for this shape; route: -1 for the plan that the library
- * compares its choice by, or one of LQ_I8_ROUTE_TC to LQ_I8_ROUTE_SPLIT. Launches nothing and goes
- * by the device as lq_gemm_i8_route does: it lets tests check the plan's bounds. out[0 .. LQ_I8_PLAN_FIELDS) receives: the route,
- * CTAs per cluster (1: none), tiles, weight rows per CTA and tokens of a tile, 128-byte chunks per
- * stage, ring stages, dynamic shared memory (bytes).
+/* The tiles of the tensor-core routes for this shape; route: one of LQ_I8_ROUTE_TC to
+ * LQ_I8_ROUTE_SPLIT, or -1 for the fastest of them by the library's estimate, which lq_gemm_i8 runs
+ * unless it takes the GEMV. Launches nothing and goes by the device as lq_gemm_i8_route does: it lets
+ * tests check the plan's bounds. out[0 .. LQ_I8_PLAN_FIELDS) receives: the route, CTAs per cluster
+ * (1: none), tiles, weight rows per CTA and tokens of a tile, 128-byte chunks per stage, ring stages,
+ * dynamic shared memory (bytes).
  * Errors: LQ_EINVAL on invalid sizes, a route without tiles or a null out. */
 #define LQ_I8_PLAN_FIELDS 8
 LQ_API lq_status lq_gemm_i8_plan(int32_t batch, int32_t K, int32_t N, int32_t route, int64_t* out);
